@@ -615,3 +615,9 @@ def fp8_grouped_gemm_wgrad(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, s
                                      _ptr(c), c.stride(1), _stream(a.device, stream))
     _check(st, "fp8_grouped_gemm_wgrad")
     return c
+
+
+# the operators around the linear layers (include/fp8q_ops.h)
+from .operators import (OPS_SYMBOLS, STATE_E4M3, STATE_F32, AdamWPlan, fp8q_adamw_multi_step,  # noqa: E402,F401
+                        fp8q_adamw_plan, fp8q_int8_gemm, fp8q_int8_quant_rows, fp8q_layer_norm_backward,
+                        fp8q_layer_norm_forward)

@@ -25,7 +25,8 @@ FLAGS = ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
          "-Wno-unused-command-line-argument"]
 
-SOURCES = ["api.hip", "check.hip", "quant.hip", "quant_transpose.hip", "gemm.hip", "gemm_nk.hip", "gemm_w4.hip", "adam.hip"]
+SOURCES = ["api.hip", "check.hip", "quant.hip", "quant_transpose.hip", "gemm.hip", "gemm_nk.hip", "gemm_w4.hip", "adam.hip",
+           "ops_api.hip", "layer_norm.hip", "adamw_multi.hip", "int8_quant.hip", "int8_gemm.hip"]
 
 
 def _compile(src: str, obj: str) -> None:

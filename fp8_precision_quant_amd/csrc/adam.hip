@@ -20,6 +20,7 @@
 // A workgroup of 256 threads covers 16 blocks per step and runs kAdamUnroll
 // steps with all loads issued first.  The pass is HBM-bound (about 14 bytes
 // per parameter with a bf16 gradient).
+#include "adam_math.h"
 #include "fp8q_device.h"
 #include "fp8q_internal.h"
 
@@ -28,19 +29,6 @@ namespace fp8q {
 constexpr int kAdamThreads = 256;
 constexpr int kAdamUnroll = 2;
 constexpr int kAdamBlocksPerWg = (kAdamThreads / 16) * kAdamUnroll;
-
-typedef float v2f __attribute__((ext_vector_type(2)));
-
-// eight E4M3 codes (little-endian in lo, hi) -> fp32 values (exact)
-__device__ __forceinline__ void decode8(uint32_t lo, uint32_t hi, float v[8])
-{
-    const v2f a = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo, false);
-    const v2f b = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo, true);
-    const v2f c = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi, false);
-    const v2f d = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi, true);
-    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
-    v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
-}
 
 template <typename G>
 __device__ __forceinline__ void load_grad8(const G* g, int64_t i0, int64_t n, float v[8]);
@@ -134,24 +122,9 @@ __global__ __launch_bounds__(kAdamThreads) void adam_fp8_kernel(
         float mx = 0.0f, vx = 0.0f;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float pi = L[u].p[k] * a.decay;
-            const float t0 = a.b1 * L[u].m[k];
-            const float t1 = a.omb1 * L[u].g[k];
-            const float mi = t0 + t1;
-            const float t2 = a.b2 * L[u].v[k];
-            const float t3 = a.omb2 * L[u].g[k];
-            const float t4 = t3 * L[u].g[k];
-            const float vi = t2 + t4;
-            const float r = __builtin_sqrtf(vi);
-            const float q = r / a.bc2_sqrt;
-            const float den = q + a.eps;
-            const float upd = mi / den;
-            const float w = a.step_size * upd;
-            L[u].p[k] = pi - w;
-            L[u].m[k] = mi;
-            L[u].v[k] = vi;
-            mx = fmaxf(mx, fabsf(mi));
-            vx = fmaxf(vx, fabsf(vi));
+            adam_update(L[u].p[k], L[u].g[k], L[u].m[k], L[u].v[k], a);
+            mx = fmaxf(mx, fabsf(L[u].m[k]));
+            vx = fmaxf(vx, fabsf(L[u].v[k]));
         }
         // block amax within the 16-lane row (rows past the end hold zeros)
         const TileScale tm = make_scale(dpp_max16(mx));

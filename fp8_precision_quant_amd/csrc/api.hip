@@ -4,63 +4,15 @@
 // enqueues anything, never allocates or synchronizes (except in the debug
 // mode FP8Q_CHECK=1), and reports a pending launch error as FP8Q_ERR_LAUNCH.  Operation semantics are documented in
 // include/fp8q.h.
-#include <atomic>
-#include <cmath>
-#include <cstring>
-
+#include "api_common.h"
 #include "fp8q_internal.h"
 
 namespace {
 
-constexpr int64_t kTile = 128;
-constexpr int64_t kMaxIndex = (int64_t)1 << 31;
+using namespace fp8q::host;
+
 // grouped GEMMs keep the group offsets in LDS
 constexpr int64_t kMaxGroups = 1024;
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int elem_size(int dtype) { return dtype == FP8Q_BF16 ? 2 : 4; }
-
-bool dtype_ok(int d) { return d == FP8Q_F32 || d == FP8Q_BF16; }
-
-// Per-device cache: 0 = unknown, 1 = gfx950, 2 = other / query failed.
-std::atomic<int> g_arch_state[64];
-
-int check_device()
-{
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) {
-        (void)hipGetLastError();
-        return FP8Q_ERR_DEVICE;
-    }
-    if (dev >= 64) return FP8Q_ERR_DEVICE;
-    int st = g_arch_state[dev].load(std::memory_order_acquire);
-    if (st == 0) {
-        hipDeviceProp_t prop;
-        if (hipGetDeviceProperties(&prop, dev) != hipSuccess) {
-            (void)hipGetLastError();
-            st = 2;
-        } else {
-            st = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-        }
-        g_arch_state[dev].store(st, std::memory_order_release);
-    }
-    return st == 1 ? FP8Q_OK : FP8Q_ERR_DEVICE;
-}
-
-// A pending launch error; with FP8Q_CHECK=1 the stream is also synchronized
-// so that an error of the work itself is reported by the call that enqueued it.
-int launch_status(hipStream_t stream)
-{
-    if (hipGetLastError() != hipSuccess) return FP8Q_ERR_LAUNCH;
-    if (fp8q::debug_checks_enabled() && hipStreamSynchronize(stream) != hipSuccess) {
-        (void)hipGetLastError();
-        return FP8Q_ERR_LAUNCH;
-    }
-    return FP8Q_OK;
-}
 
 // FP8Q_CHECK=1: the group offsets are checked on the device first.
 int offsets_status(const int32_t* offsets, int64_t G, int64_t M_pad, hipStream_t stream)
@@ -232,9 +184,7 @@ int fp8_adam_step(int64_t n, float* p, const void* g, int g_dtype, uint8_t* mq, 
                   double weight_decay, int64_t step, hipStream_t stream)
 {
     if (!dtype_ok(g_dtype)) return FP8Q_ERR_UNSUPPORTED;
-    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || step < 1 ||
-        !std::isfinite(lr) || !std::isfinite(eps) || !std::isfinite(weight_decay))
-        return FP8Q_ERR_UNSUPPORTED;
+    if (!adam_hyper_ok(lr, beta1, beta2, eps, weight_decay, step)) return FP8Q_ERR_UNSUPPORTED;
     if (n < 0) return FP8Q_ERR_SHAPE;
     if (n == 0) return FP8Q_OK;
     if (!p || !g || !mq || !ms || !vq || !vs) return FP8Q_ERR_NULL;
@@ -244,16 +194,7 @@ int fp8_adam_step(int64_t n, float* p, const void* g, int g_dtype, uint8_t* mq, 
         return FP8Q_ERR_ALIGN;
     int st = check_device();
     if (st != FP8Q_OK) return st;
-    // derived scalars: computed in double, each rounded once to fp32
-    fp8q::AdamScalars a;
-    a.b1 = (float)beta1;
-    a.b2 = (float)beta2;
-    a.omb1 = (float)(1.0 - beta1);
-    a.omb2 = (float)(1.0 - beta2);
-    a.decay = (float)(1.0 - lr * weight_decay);
-    a.step_size = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
-    a.bc2_sqrt = (float)std::sqrt(1.0 - std::pow(beta2, (double)step));
-    a.eps = (float)eps;
+    const fp8q::AdamScalars a = adam_scalars(lr, beta1, beta2, eps, weight_decay, step);
     fp8q::launch_adam_fp8(n, p, g, g_dtype, mq, ms, vq, vs, a, stream);
     return launch_status(stream);
 }

@@ -1,0 +1,200 @@
+// C ABI of the operators around the linear layers (include/fp8q_ops.h):
+// argument validation, device check, dispatch.
+#include <cmath>
+
+#include "api_common.h"
+#include "ops_internal.h"
+
+namespace {
+
+using namespace fp8q::host;
+
+bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
+
+// sizes far beyond any memory, refused before they are multiplied
+constexpr int64_t kMaxSize = (int64_t)1 << 40;
+// |sum of K products of codes| <= K * 128^2 stays inside int32
+constexpr int64_t kMaxInt8K = 131071;
+// a tile's rows are addressed with 32-bit offsets
+constexpr int64_t kMaxInt8Ld = (int64_t)1 << 23;
+
+}  // namespace
+
+extern "C" {
+
+int fp8q_layer_norm_forward(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, const void* w,
+                            const void* b, int w_dtype, double eps, void* y, int64_t ldy, float* mean, float* rstd,
+                            hipStream_t stream)
+{
+    if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype)) return FP8Q_ERR_UNSUPPORTED;
+    if (!std::isfinite(eps) || eps < 0.0) return FP8Q_ERR_UNSUPPORTED;
+    if (rows < 0 || cols < 0 || rows > kMaxSize || cols > kMaxSize) return FP8Q_ERR_SHAPE;
+    if (rows == 0) return FP8Q_OK;
+    if (cols == 0 || ldx < cols || ldy < cols) return FP8Q_ERR_SHAPE;
+    if (!x || !y) return FP8Q_ERR_NULL;
+    const int xe = elem_size(x_dtype), we = elem_size(w_dtype);
+    if (!aligned(x, xe) || !aligned(y, xe) || !aligned(w, we) || !aligned(b, we) || !aligned(mean, 4) ||
+        !aligned(rstd, 4))
+        return FP8Q_ERR_ALIGN;
+    const int st = check_device();
+    if (st != FP8Q_OK) return st;
+    fp8q::launch_layer_norm_forward(x, x_dtype, rows, cols, ldx, w, b, w_dtype, (float)eps, y, ldy, mean, rstd,
+                                    stream);
+    return launch_status(stream);
+}
+
+int64_t fp8q_layer_norm_backward_workspace(int64_t rows, int64_t cols)
+{
+    if (rows < 0 || cols < 0 || rows > kMaxSize || cols > kMaxSize) return 0;
+    return fp8q::layer_norm_backward_workspace(rows, cols);
+}
+
+int fp8q_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int x_dtype, int64_t rows, int64_t cols,
+                             int64_t ldx, const float* mean, const float* rstd, const void* w, int w_dtype, void* dx,
+                             int64_t lddx, void* dw, void* db, void* workspace, int64_t workspace_bytes,
+                             hipStream_t stream)
+{
+    if (!dtype_ok(x_dtype) || !dtype_ok(w_dtype)) return FP8Q_ERR_UNSUPPORTED;
+    if (rows < 0 || cols < 0 || rows > kMaxSize || cols > kMaxSize) return FP8Q_ERR_SHAPE;
+    if (cols == 0) return rows == 0 ? FP8Q_OK : FP8Q_ERR_SHAPE;
+    if (!dx && !dw && !db) return FP8Q_OK;
+    if (rows > 0 && (ldx < cols || lddy < cols || (dx && lddx < cols))) return FP8Q_ERR_SHAPE;
+    if (rows > 0 && (!x || !dy || !mean || !rstd)) return FP8Q_ERR_NULL;
+    if ((dw || db) && !workspace) return FP8Q_ERR_NULL;
+    if ((dw || db) && workspace_bytes < fp8q::layer_norm_backward_workspace(rows, cols)) return FP8Q_ERR_SHAPE;
+    const int xe = elem_size(x_dtype), we = elem_size(w_dtype);
+    if (!aligned(x, xe) || !aligned(dy, xe) || !aligned(dx, xe) || !aligned(w, we) || !aligned(dw, we) ||
+        !aligned(db, we) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned16(workspace))
+        return FP8Q_ERR_ALIGN;
+    if (rows == 0 && !dw && !db) return FP8Q_OK;
+    const int st = check_device();
+    if (st != FP8Q_OK) return st;
+    fp8q::launch_layer_norm_backward(dy, lddy, x, x_dtype, rows, cols, ldx, mean, rstd, w, w_dtype, dx, lddx, dw, db,
+                                     static_cast<float*>(workspace), stream);
+    return launch_status(stream);
+}
+
+int64_t fp8q_adamw_table_bytes(int64_t count, const int64_t* n)
+{
+    if (count < 0 || count > kMaxIndex - 1 || (count > 0 && !n)) return -1;
+    int64_t chunks = 0, blocks = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (n[i] < 0 || n[i] > kMaxSize) return -1;
+        const int64_t nb = cdiv(n[i], kTile);
+        if (nb >= kMaxIndex) return -1;
+        chunks += cdiv(nb, fp8q::kAdamwChunk);
+        blocks += nb;
+        if (blocks >= kMaxSize) return -1;
+    }
+    return (int64_t)sizeof(fp8q::AdamwHeader) + count * (int64_t)sizeof(fp8q::AdamwTensor) +
+           chunks * (int64_t)sizeof(fp8q::AdamwChunk);
+}
+
+int fp8q_adamw_table_fill(int64_t count, const int64_t* n, void* table, int64_t bytes)
+{
+    const int64_t need = fp8q_adamw_table_bytes(count, n);
+    if (need < 0 || bytes != need) return FP8Q_ERR_SHAPE;
+    if (!table) return FP8Q_ERR_NULL;
+    if (!aligned(table, 8)) return FP8Q_ERR_ALIGN;
+    auto* h = static_cast<fp8q::AdamwHeader*>(table);
+    auto* t = reinterpret_cast<fp8q::AdamwTensor*>(h + 1);
+    auto* c = reinterpret_cast<fp8q::AdamwChunk*>(t + count);
+    int64_t block = 0, chunk = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        const int64_t nb = cdiv(n[i], kTile);
+        t[i] = {n[i], block, chunk, 0};
+        for (int64_t k = 0; k < nb; k += fp8q::kAdamwChunk) c[chunk++] = {(int32_t)i, (uint32_t)k};
+        block += nb;
+    }
+    *h = {fp8q::kAdamwMagic, count, chunk, need};
+    return FP8Q_OK;
+}
+
+int fp8q_adamw_multi_step(const void* table_host, const void* table_device, float* const* p, const void* const* g,
+                          int g_dtype, int state_kind, void* m, float* ms, void* v, float* vs, double lr, double beta1,
+                          double beta2, double eps, double weight_decay, int64_t step, hipStream_t stream)
+{
+    if (!dtype_ok(g_dtype)) return FP8Q_ERR_UNSUPPORTED;
+    if (state_kind != FP8Q_STATE_F32 && state_kind != FP8Q_STATE_E4M3) return FP8Q_ERR_UNSUPPORTED;
+    if (!adam_hyper_ok(lr, beta1, beta2, eps, weight_decay, step)) return FP8Q_ERR_UNSUPPORTED;
+    if (!table_host) return FP8Q_ERR_NULL;
+    if (!aligned(table_host, 8)) return FP8Q_ERR_ALIGN;
+    const auto* h = static_cast<const fp8q::AdamwHeader*>(table_host);
+    if (h->magic != fp8q::kAdamwMagic) return FP8Q_ERR_SHAPE;
+    const auto* t = reinterpret_cast<const fp8q::AdamwTensor*>(h + 1);
+    if (h->chunks == 0) return FP8Q_OK;
+    const bool e4m3 = state_kind == FP8Q_STATE_E4M3;
+    if (!table_device || !p || !g || !m || !v || (e4m3 && (!ms || !vs))) return FP8Q_ERR_NULL;
+    if (!aligned(table_device, 8) || !aligned16(m) || !aligned16(v) || !aligned(ms, 4) || !aligned(vs, 4))
+        return FP8Q_ERR_ALIGN;
+    const int ge = elem_size(g_dtype);
+    for (int64_t i = 0; i < h->count; ++i) {
+        if (!g[i] || t[i].n == 0) continue;
+        if (!p[i]) return FP8Q_ERR_NULL;
+        if (!aligned(p[i], 4) || !aligned(g[i], ge)) return FP8Q_ERR_ALIGN;
+    }
+    // the grid's threads are counted in 32 bits
+    constexpr int64_t kMaxChunks = (int64_t)1 << 23;
+    const fp8q::AdamScalars a = adam_scalars(lr, beta1, beta2, eps, weight_decay, step);
+    const int st = check_device();
+    if (st != FP8Q_OK) return st;
+    for (int64_t t0 = 0; t0 < h->count; t0 += fp8q::kAdamwPerLaunch) {
+        const int64_t count = h->count - t0 < fp8q::kAdamwPerLaunch ? h->count - t0 : fp8q::kAdamwPerLaunch;
+        const int64_t end = t0 + count < h->count ? t[t0 + count].chunk0 : h->chunks;
+        for (int64_t c0 = t[t0].chunk0; c0 < end; c0 += kMaxChunks)
+            fp8q::launch_adamw_multi(table_device, h->count, (int)t0, (int)count, c0,
+                                     end - c0 < kMaxChunks ? end - c0 : kMaxChunks, p, g, g_dtype, state_kind, m, ms,
+                                     v, vs, a, stream);
+    }
+    return launch_status(stream);
+}
+
+int fp8q_int8_quant_rows(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx, int8_t* q, int64_t ldq,
+                         float* s, hipStream_t stream)
+{
+    if (!dtype_ok(x_dtype)) return FP8Q_ERR_UNSUPPORTED;
+    if (rows < 0 || cols < 0 || rows > kMaxSize || cols > kMaxSize) return FP8Q_ERR_SHAPE;
+    if (rows == 0) return FP8Q_OK;
+    if (ldx < cols || ldq < cols) return FP8Q_ERR_SHAPE;
+    if (!s || (cols > 0 && (!x || !q))) return FP8Q_ERR_NULL;
+    if (!aligned(x, elem_size(x_dtype)) || !aligned16(q) || ldq % 16 || !aligned(s, 4)) return FP8Q_ERR_ALIGN;
+    const int st = check_device();
+    if (st != FP8Q_OK) return st;
+    fp8q::launch_int8_quant_rows(x, x_dtype, rows, cols, ldx, q, ldq, s, stream);
+    return launch_status(stream);
+}
+
+int64_t fp8q_int8_gemm_workspace(int64_t M, int64_t N, int64_t K)
+{
+    if (M <= 0 || N <= 0 || K <= 0 || M >= kMaxIndex || N >= kMaxIndex || K > kMaxInt8K) return 0;
+    return fp8q::int8_gemm_workspace(M, N, K);
+}
+
+int fp8q_int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* sa, const int8_t* b,
+                   int64_t ldb, const float* sb, const float* bias, void* c, int64_t ldc, int c_dtype,
+                   void* workspace, int64_t workspace_bytes, hipStream_t stream)
+{
+    if (!dtype_ok(c_dtype)) return FP8Q_ERR_UNSUPPORTED;
+    if (M < 0 || N < 0 || K < 0 || M >= kMaxIndex || N >= kMaxIndex) return FP8Q_ERR_SHAPE;
+    if (M == 0 || N == 0) return FP8Q_OK;
+    if (K > kMaxInt8K) return FP8Q_ERR_UNSUPPORTED;
+    if (!c || (K > 0 && (!a || !sa || !b || !sb))) return FP8Q_ERR_NULL;
+    if (lda < K || ldb < K || ldc < N || ldc > kMaxSize) return FP8Q_ERR_SHAPE;
+    if (lda >= kMaxInt8Ld || ldb >= kMaxInt8Ld) return FP8Q_ERR_UNSUPPORTED;
+    // (a launch's threads are counted in 32 bits)
+    if (cdiv(M, 64) * cdiv(N, 64) >= ((int64_t)1 << 23)) return FP8Q_ERR_UNSUPPORTED;
+    const int64_t need = fp8q::int8_gemm_workspace(M, N, K);
+    if (need > 0 && !workspace) return FP8Q_ERR_NULL;
+    if (need > 0 && workspace_bytes < need) return FP8Q_ERR_SHAPE;
+    if (!aligned16(c) || (ldc * elem_size(c_dtype)) % 16 || !aligned(bias, 4) || !aligned16(workspace))
+        return FP8Q_ERR_ALIGN;
+    if (K > 0 && (!aligned16(a) || !aligned16(b) || lda % 16 || ldb % 16 || !aligned(sa, 4) || !aligned(sb, 4)))
+        return FP8Q_ERR_ALIGN;
+    const int st = check_device();
+    if (st != FP8Q_OK) return st;
+    fp8q::launch_int8_gemm(M, N, K, a, lda, sa, b, ldb, sb, bias, c, ldc, c_dtype, static_cast<int32_t*>(workspace),
+                           stream);
+    return launch_status(stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,341 @@
+"""Operators around the FP8 linear layers: layer norm forward and backward,
+the AdamW step over many tensors, the per-row int8 quantizer and the int8
+product with a scale per token and per output channel.
+
+Binding of ``include/fp8q_ops.h`` in the manner of the package: the functions
+carry the C names, check their tensors (ValueError before any launch), allocate
+the outputs that are not given and enqueue the kernels on the current stream
+(or on ``stream``).  Rows may have any length, stride and element alignment
+where the header says so.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import List, Optional, Sequence, Tuple
+
+import torch
+
+from . import (BF16, F32, TILE, Fp8qError, OK, _cdiv, _device, _dtype, _empty_aligned, _ld, _lib, _on, _ptr, _shape)
+
+STATE_F32, STATE_E4M3 = 0, 1
+
+_i64, _int, _p, _d = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_double
+_lib.fp8q_layer_norm_forward.argtypes = [_p, _int, _i64, _i64, _i64, _p, _p, _int, _d, _p, _i64, _p, _p, _p]
+_lib.fp8q_layer_norm_backward_workspace.argtypes = [_i64, _i64]
+_lib.fp8q_layer_norm_backward.argtypes = [_p, _i64, _p, _int, _i64, _i64, _i64, _p, _p, _p, _int, _p, _i64, _p, _p,
+                                          _p, _i64, _p]
+_lib.fp8q_adamw_table_bytes.argtypes = [_i64, _p]
+_lib.fp8q_adamw_table_fill.argtypes = [_i64, _p, _p, _i64]
+_lib.fp8q_adamw_multi_step.argtypes = [_p, _p, _p, _p, _int, _int, _p, _p, _p, _p, _d, _d, _d, _d, _d, _i64, _p]
+_lib.fp8q_int8_quant_rows.argtypes = [_p, _int, _i64, _i64, _i64, _p, _i64, _p, _p]
+_lib.fp8q_int8_gemm_workspace.argtypes = [_i64, _i64, _i64]
+_lib.fp8q_int8_gemm.argtypes = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _p, _p, _i64, _int, _p, _i64, _p]
+for _f in ("fp8q_layer_norm_forward", "fp8q_layer_norm_backward", "fp8q_adamw_table_fill", "fp8q_adamw_multi_step",
+           "fp8q_int8_quant_rows", "fp8q_int8_gemm"):
+    getattr(_lib, _f).restype = _int
+for _f in ("fp8q_layer_norm_backward_workspace", "fp8q_adamw_table_bytes", "fp8q_int8_gemm_workspace"):
+    getattr(_lib, _f).restype = _i64
+
+# the functions of include/fp8q_ops.h
+OPS_SYMBOLS = ("fp8q_layer_norm_forward", "fp8q_layer_norm_backward_workspace", "fp8q_layer_norm_backward",
+               "fp8q_adamw_table_bytes", "fp8q_adamw_table_fill", "fp8q_adamw_multi_step", "fp8q_int8_quant_rows",
+               "fp8q_int8_gemm_workspace", "fp8q_int8_gemm")
+
+_FLOATS = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+def _float_code(name: str, t: torch.Tensor) -> int:
+    code = _FLOATS.get(t.dtype)
+    if code is None:
+        raise ValueError("%s must be torch.bfloat16 or torch.float32, got %s" % (name, t.dtype))
+    return code
+
+
+def _vector(name: str, t: Optional[torch.Tensor], n: int, dtype: torch.dtype) -> None:
+    """A contiguous vector of n elements of dtype (or None)."""
+    if t is not None and (t.shape != (n,) or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s vector of %d elements, got %s %s" %
+                         (name, dtype, n, t.dtype, tuple(t.shape)))
+
+
+class _Call:
+    """Where a call runs: its device and stream.  Memory allocated for the call belongs to the current stream;
+    where the work goes to another one, the allocator is told (``keep``)."""
+    __slots__ = ("dev", "handle", "other", "guard")
+
+    def __init__(self, first: torch.Tensor, stream):
+        self.dev = first.device
+        self.other = None
+        if stream is None:
+            if self.dev.type != "cuda":
+                _device(first, stream)      # raises
+            self.handle = torch.cuda.current_stream(self.dev).cuda_stream
+        else:
+            self.dev = _device(first, stream)
+            self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            if self.handle != torch.cuda.current_stream(self.dev).cuda_stream:
+                self.other = stream if isinstance(stream, torch.cuda.Stream) else \
+                    torch.cuda.ExternalStream(self.handle, device=self.dev)
+        # the library launches on the thread's current device
+        self.guard = None
+        if self.dev.index is not None and torch.cuda.current_device() != self.dev.index:
+            self.guard = torch.cuda.device(self.dev)
+
+    def __call__(self, fn, where: str, *args) -> None:
+        if self.guard is None:
+            st = fn(*args, self.handle)
+        else:
+            with self.guard:
+                st = fn(*args, self.handle)
+        if st != OK:
+            raise Fp8qError(st, where)
+
+    def keep(self, *tensors: Optional[torch.Tensor]) -> None:
+        if self.other is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.other)
+
+
+# ---------------------------------------------------------------------------
+# layer norm
+# ---------------------------------------------------------------------------
+
+def fp8q_layer_norm_forward(x: torch.Tensor, w: Optional[torch.Tensor] = None, b: Optional[torch.Tensor] = None,
+                            eps: float = 1e-5, y: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                            rstd: Optional[torch.Tensor] = None, stream=None
+                            ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Layer norm of the rows of ``x[rows, cols]`` (bf16 or fp32): ``(y, mean, rstd)``.
+
+    ``w`` and ``b`` are vectors of ``cols`` elements, bf16 or fp32 and of one type; None stands for ones and zeros.
+    ``y`` has x's type, its default row stride is rounded up to 16 bytes (as the quantizers read it); ``mean`` and
+    ``rstd`` are fp32, as ``fp8q_layer_norm_backward`` takes them."""
+    rows, cols = x.shape
+    call = _Call(x, stream)
+    xd = _float_code("x", x)
+    wt = w if w is not None else b
+    wd = F32 if wt is None else _float_code("w", wt)
+    if wt is not None:
+        _vector("w", w, cols, wt.dtype)
+        _vector("b", b, cols, wt.dtype)
+    if y is None:
+        y = _empty_aligned(rows, cols, x.dtype, x.device, 8 if xd == BF16 else 4)
+    if mean is None:
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _on(call.dev, x=x, w=w, b=b, y=y, mean=mean, rstd=rstd)
+    _dtype("y", y, (x.dtype,))
+    _shape("y", y, (rows, cols))
+    _vector("mean", mean, rows, torch.float32)
+    _vector("rstd", rstd, rows, torch.float32)
+    call(_lib.fp8q_layer_norm_forward, "fp8q_layer_norm_forward", x.data_ptr(), xd, rows, cols, _ld(x), _ptr(w),
+         _ptr(b), wd, eps, y.data_ptr(), _ld(y), mean.data_ptr(), rstd.data_ptr())
+    call.keep(y, mean, rstd)
+    return y, mean, rstd
+
+
+def fp8q_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                             w: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                             dw: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None, stream=None
+                             ) -> Tuple[torch.Tensor, Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """Gradients of the layer norm: ``(dx, dw, db)`` from ``dy`` and the forward pass's ``x``, ``mean``, ``rstd`` and
+    ``w``.  ``dx`` has x's type, ``dw`` and ``db`` have w's.  Without weights (``w`` None) dw and db are computed only
+    where given (bf16 or fp32 vectors of one type), else returned as None."""
+    rows, cols = x.shape
+    call = _Call(x, stream)
+    xd = _float_code("x", x)
+    wt = w if w is not None else dw if dw is not None else db
+    wd = F32 if wt is None else _float_code("w", wt)
+    if dx is None:
+        dx = _empty_aligned(rows, cols, x.dtype, x.device, 8 if xd == BF16 else 4)
+    if w is not None:
+        if dw is None:
+            dw = torch.empty(cols, dtype=w.dtype, device=x.device)
+        if db is None:
+            db = torch.empty(cols, dtype=w.dtype, device=x.device)
+    _on(call.dev, dy=dy, x=x, mean=mean, rstd=rstd, w=w, dx=dx, dw=dw, db=db)
+    _dtype("dy", dy, (x.dtype,))
+    _dtype("dx", dx, (x.dtype,))
+    _shape("dy", dy, (rows, cols))
+    _shape("dx", dx, (rows, cols))
+    _vector("mean", mean, rows, torch.float32)
+    _vector("rstd", rstd, rows, torch.float32)
+    if wt is not None:
+        _vector("w", w, cols, wt.dtype)
+        _vector("dw", dw, cols, wt.dtype)
+        _vector("db", db, cols, wt.dtype)
+    ws, nws = None, 0
+    if wt is not None:
+        nws = _lib.fp8q_layer_norm_backward_workspace(rows, cols)
+        ws = torch.empty(nws, dtype=torch.uint8, device=x.device)
+    call(_lib.fp8q_layer_norm_backward, "fp8q_layer_norm_backward", dy.data_ptr(), _ld(dy), x.data_ptr(), xd, rows,
+         cols, _ld(x), mean.data_ptr(), rstd.data_ptr(), _ptr(w), wd, dx.data_ptr(), _ld(dx), _ptr(dw), _ptr(db),
+         _ptr(ws), nws)
+    call.keep(dx, dw, db, ws)
+    return dx, dw, db
+
+
+# ---------------------------------------------------------------------------
+# AdamW over many tensors
+# ---------------------------------------------------------------------------
+
+class AdamWPlan:
+    """The parameters of ``fp8q_adamw_multi_step`` and the layout of their moments (made by ``fp8q_adamw_plan``).
+
+    ``moments`` are the caller's tensors, updated in place: (m, v) in fp32, or (mq, ms, vq, vs) as E4M3 codes and
+    scales; tensor i's begin at element ``128 * blocks[i]`` (and scale ``blocks[i]``)."""
+
+    def __init__(self, params: Sequence[torch.Tensor], kind: int, moments: Tuple[torch.Tensor, ...]):
+        params = list(params)
+        if kind not in (STATE_F32, STATE_E4M3):
+            raise ValueError("unknown moment state %r" % (kind,))
+        if not params:
+            raise ValueError("no parameters")
+        dev = _device(params[0], None)
+        for i, p in enumerate(params):
+            _on(dev, **{"params[%d]" % i: p})
+            if p.dtype != torch.float32 or not p.is_contiguous():
+                raise ValueError("params[%d] must be contiguous torch.float32, got %s" % (i, p.dtype))
+        self.params: List[torch.Tensor] = params
+        self.kind = kind
+        self.sizes = [p.numel() for p in params]
+        self.blocks = [0]
+        for n in self.sizes:
+            self.blocks.append(self.blocks[-1] + _cdiv(n, TILE))
+        B = self.blocks[-1]
+        want = [(torch.float32, B * TILE)] * 2 if kind == STATE_F32 else \
+            [(torch.uint8, B * TILE), (torch.float32, B)] * 2
+        if moments is None:
+            moments = tuple(torch.zeros(n, dtype=dt, device=dev) for dt, n in want)
+        moments = tuple(moments)
+        if len(moments) != len(want):
+            raise ValueError("expected %d moment tensors, got %d" % (len(want), len(moments)))
+        for i, (t, (dt, n)) in enumerate(zip(moments, want)):
+            _on(dev, **{"moments[%d]" % i: t})
+            _vector("moments[%d]" % i, t, n, dt)
+        self.moments = moments
+        self.device = dev
+        count = len(params)
+        arr = (_i64 * count)(*self.sizes)
+        nbytes = _lib.fp8q_adamw_table_bytes(count, arr)
+        if nbytes < 0:
+            raise ValueError("the parameter list is too large")
+        self._host = torch.empty(nbytes, dtype=torch.uint8)
+        st = _lib.fp8q_adamw_table_fill(count, arr, self._host.data_ptr(), nbytes)
+        if st != OK:
+            raise Fp8qError(st, "fp8q_adamw_table_fill")
+        self._table = self._host.to(dev)
+        torch.cuda.current_stream(dev).synchronize()     # a step may run on any stream
+        self._at = [p.data_ptr() for p in params]
+        self._p = (_p * count)(*self._at)
+        self._vectors = _p * count
+
+
+def fp8q_adamw_plan(params: Sequence[torch.Tensor], state_kind: int = STATE_E4M3, moments: Optional[tuple] = None
+                    ) -> AdamWPlan:
+    """Lay out the AdamW step of ``params`` (contiguous fp32 tensors of any shapes, stepped in place).
+
+    ``state_kind``: STATE_E4M3 (codes and one fp32 scale per 128 elements) or STATE_F32.  ``moments`` are flat
+    buffers over all tensors, each tensor's part padded to a multiple of 128 elements: ``(m, v)`` fp32 ``[128 B]``, or
+    ``(mq, ms, vq, vs)`` uint8 ``[128 B]`` and fp32 ``[B]`` with B the number of 128-element blocks; fresh (zero)
+    ones are allocated if None.  The plan is made once; a parameter that moves in memory needs a new one."""
+    return AdamWPlan(params, state_kind, moments)
+
+
+def fp8q_adamw_multi_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor]], lr: float, beta1: float = 0.9,
+                          beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0, step: int = 1,
+                          stream=None) -> None:
+    """One AdamW step (the arithmetic of ``fp8_adam_step``) on all of the plan's parameters, in place.
+
+    ``grads``: one contiguous tensor per parameter with as many elements, all bf16 or all fp32; a parameter whose
+    entry is None is left as it is.  In a captured graph the hyperparameters, the step number and the addresses of
+    this call are replayed."""
+    if not isinstance(plan, AdamWPlan):
+        raise ValueError("plan must come from fp8q_adamw_plan")
+    if len(grads) != len(plan.sizes):
+        raise ValueError("%d gradients for %d parameters" % (len(grads), len(plan.sizes)))
+    call = _Call(plan.params[0], stream)
+    dev = plan.device
+    if [p.data_ptr() for p in plan.params] != plan._at:
+        raise ValueError("a parameter has moved in memory since the plan was made")
+    gdtype, ptrs = None, []
+    for i, (g, n) in enumerate(zip(grads, plan.sizes)):
+        if g is None:
+            ptrs.append(None)
+            continue
+        if g.numel() != n or not g.is_contiguous() or g.device != dev:
+            raise ValueError("grads[%d] must be contiguous with %d elements on %s, got %s on %s" %
+                             (i, n, dev, tuple(g.shape), g.device))
+        if gdtype is None:
+            gdtype = g.dtype
+            gd = _float_code("grads[%d]" % i, g)
+        elif g.dtype != gdtype:
+            raise ValueError("gradients must have one type, got %s and %s" % (gdtype, g.dtype))
+        ptrs.append(g.data_ptr())
+    if gdtype is None:
+        return
+    if plan.kind == STATE_F32:
+        m, v = plan.moments
+        ms = vs = None
+    else:
+        m, ms, v, vs = plan.moments
+    call(_lib.fp8q_adamw_multi_step, "fp8q_adamw_multi_step", plan._host.data_ptr(), plan._table.data_ptr(), plan._p,
+         plan._vectors(*ptrs), gd, plan.kind, m.data_ptr(), _ptr(ms), v.data_ptr(), _ptr(vs), lr, beta1, beta2, eps,
+         weight_decay, step)
+    call.keep(plan._table)
+
+
+# ---------------------------------------------------------------------------
+# int8
+# ---------------------------------------------------------------------------
+
+def fp8q_int8_quant_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None,
+                         stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """int8 codes ``q[rows, cols]`` (row stride a multiple of 16) and fp32 scales ``s[rows]`` of ``x`` (bf16 or
+    fp32): s = max |x| / 127 of the row, q = rint(x / s)."""
+    rows, cols = x.shape
+    call = _Call(x, stream)
+    xd = _float_code("x", x)
+    if q is None:
+        q = _empty_aligned(rows, cols, torch.int8, x.device, 16)
+    if s is None:
+        s = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _on(call.dev, x=x, q=q, s=s)
+    _dtype("q", q, (torch.int8,))
+    _shape("q", q, (rows, cols))
+    _vector("s", s, rows, torch.float32)
+    call(_lib.fp8q_int8_quant_rows, "fp8q_int8_quant_rows", x.data_ptr(), xd, rows, cols, _ld(x), q.data_ptr(),
+         _ld(q), s.data_ptr())
+    call.keep(q, s)
+    return q, s
+
+
+def fp8q_int8_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor,
+                   bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                   c: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """``C[M, N] = (a b^T) * sa[:, None] * sb[None, :] + bias`` of int8 codes ``a[M, K]`` and ``b[N, K]`` with fp32
+    scales ``sa[M]`` (tokens) and ``sb[N]`` (output channels) and an fp32 ``bias[N]``; bf16 or fp32 out."""
+    M, K = a.shape
+    N, Kb = b.shape
+    if Kb != K:
+        raise ValueError("contraction sizes differ: a %s, b %s" % (tuple(a.shape), tuple(b.shape)))
+    call = _Call(a, stream)
+    if c is None:
+        if out_dtype not in _FLOATS:
+            raise ValueError("output dtype must be float32 or bfloat16")
+        c = _empty_aligned(M, N, out_dtype, a.device, 4 if out_dtype == torch.float32 else 8)
+    _on(call.dev, a=a, sa=sa, b=b, sb=sb, bias=bias, c=c)
+    cd = _float_code("c", c)
+    _dtype("a", a, (torch.int8,))
+    _dtype("b", b, (torch.int8,))
+    _vector("sa", sa, M, torch.float32)
+    _vector("sb", sb, N, torch.float32)
+    _vector("bias", bias, N, torch.float32)
+    _shape("c", c, (M, N))
+    nws = _lib.fp8q_int8_gemm_workspace(M, N, K)
+    ws = torch.empty(nws, dtype=torch.uint8, device=a.device) if nws else None
+    call(_lib.fp8q_int8_gemm, "fp8q_int8_gemm", M, N, K, a.data_ptr(), _ld(a), sa.data_ptr(), b.data_ptr(), _ld(b),
+         sb.data_ptr(), _ptr(bias), c.data_ptr(), _ld(c), cd, _ptr(ws), nws)
+    call.keep(c, ws)
+    return c

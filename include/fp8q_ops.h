@@ -1,0 +1,145 @@
+/*
+ * fp8q_ops.h -- operators around the block-scaled FP8 linear layers of
+ * libfp8q.so (AMD Instinct MI355X, gfx950): layer norm forward and backward,
+ * the AdamW step over many tensors at once, the per-row int8 quantizer and
+ * the int8 matrix product with a scale per token and per output channel.
+ *
+ * The conventions of fp8q.h hold: device pointers, row strides in elements,
+ * work enqueued on `stream`, nothing allocated, synchronized or kept after a
+ * call, arguments validated on the host before any launch, FP8Q_CHECK=1
+ * reports an error of the work itself.  Where a call needs scratch memory the
+ * caller passes it and asks for its size first; its contents on entry do not
+ * matter and it is free again when the stream has finished the call.  Outputs
+ * overlap neither inputs nor each other, except where "in place" is said.
+ * Only element alignment is asked of the layer norm's rows, the quantizer's
+ * input and the parameters and gradients of AdamW (any row stride >= cols);
+ * the int8 codes and the product's output follow fp8q.h's 16-byte rule.
+ * Every result is the same, bit for bit, from call to call.
+ */
+#ifndef FP8Q_OPS_H
+#define FP8Q_OPS_H
+
+#include "fp8q.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { FP8Q_STATE_F32 = 0, FP8Q_STATE_E4M3 = 1 } fp8q_state_kind;
+
+/*
+ * fp8q_layer_norm_forward -- layer norm over the columns of X[rows][cols]:
+ *   mean = sum_c x / cols,  rstd = 1 / sqrt(sum_c (x - mean)^2 / cols + eps),
+ *   y = (x - mean) * rstd * w + b.
+ *  x, x_dtype : FP8Q_F32 or FP8Q_BF16, row stride ldx >= cols; y likewise
+ *               (the same type, row stride ldy >= cols), rounded once.
+ *  w, b       : [cols] of w_dtype; NULL stands for ones and for zeros.
+ *  mean, rstd : fp32 [rows] for the backward pass; either may be NULL.
+ * The sums are fp32, the squares taken from the mean (two passes over a row
+ * held on chip).  cols == 0 with rows > 0 (no statistics) is FP8Q_ERR_SHAPE;
+ * rows == 0 returns FP8Q_OK.  A row that holds a NaN or an infinity gives NaN
+ * in that row only.  A negative or non-finite eps is FP8Q_ERR_UNSUPPORTED.
+ */
+int fp8q_layer_norm_forward(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                            const void* w, const void* b, int w_dtype, double eps,
+                            void* y, int64_t ldy, float* mean, float* rstd, hipStream_t stream);
+
+/* Scratch bytes of fp8q_layer_norm_backward for these sizes (0 for sizes it
+ * refuses). */
+int64_t fp8q_layer_norm_backward_workspace(int64_t rows, int64_t cols);
+
+/*
+ * fp8q_layer_norm_backward -- with xh = (x - mean) * rstd and u = dy * w:
+ *   dx = rstd * (u - sum_c u / cols - xh * sum_c (u * xh) / cols),
+ *   dw = sum_rows dy * xh,  db = sum_rows dy.
+ *  dy, x, dx  : x_dtype, row strides lddy, ldx, lddx >= cols.
+ *  mean, rstd : as the forward pass stored them.
+ *  w          : as the forward pass (NULL: ones); dw and db have its type.
+ *  dx, dw, db : each may be NULL to skip it.  rows == 0 gives dw = db = 0.
+ *  workspace  : at least fp8q_layer_norm_backward_workspace(rows, cols) bytes,
+ *               16-byte aligned; may be NULL if dw and db are.
+ * Sums are fp32 in a fixed order.
+ */
+int fp8q_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int x_dtype,
+                             int64_t rows, int64_t cols, int64_t ldx, const float* mean, const float* rstd,
+                             const void* w, int w_dtype, void* dx, int64_t lddx, void* dw, void* db,
+                             void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * AdamW over many tensors: one call steps any number of fp32 parameter
+ * tensors, with the arithmetic of fp8_adam_step.  The moments of all tensors
+ * lie in one buffer each, tensor after tensor, every tensor starting on a
+ * multiple of 128 elements (its "blocks"; B = the sum of ceil(n / 128)):
+ *   FP8Q_STATE_E4M3: m, v codes [128 B] and scales ms, vs fp32 [B];
+ *   FP8Q_STATE_F32 : m, v fp32 [128 B]; ms and vs are not used.
+ * A fresh state is all zero bytes.  Elements between a tensor's end and its
+ * last block's end are neither read into a result nor written.
+ *
+ * The layout is described by a table, made once on the host for a list of
+ * sizes and copied to the device by the caller (who keeps both copies):
+ *  fp8q_adamw_table_bytes : its size for `count` tensors of n[i] elements;
+ *                           -1 if a size is negative or the list too large.
+ *  fp8q_adamw_table_fill  : writes it (`bytes` must be that size).
+ */
+int64_t fp8q_adamw_table_bytes(int64_t count, const int64_t* n);
+int fp8q_adamw_table_fill(int64_t count, const int64_t* n, void* table, int64_t bytes);
+
+/*
+ * fp8q_adamw_multi_step -- one AdamW step, in place.
+ *  table_host, table_device : the two copies of the table (8-byte aligned).
+ *  p, g    : HOST arrays of table count device pointers: fp32 parameters and
+ *            gradients of g_dtype (element alignment).  They are copied into
+ *            the launch.  A tensor whose g is NULL is left as it is, moments
+ *            included; p may be NULL only for such tensors and empty ones.
+ *  m, ms, v, vs : the moments as above, m and v 16-byte aligned.
+ *  lr .. step   : as fp8_adam_step, with the same errors.
+ * One kernel launch per 192 tensors.
+ */
+int fp8q_adamw_multi_step(const void* table_host, const void* table_device, float* const* p, const void* const* g,
+                          int g_dtype, int state_kind, void* m, float* ms, void* v, float* vs,
+                          double lr, double beta1, double beta2, double eps, double weight_decay, int64_t step,
+                          hipStream_t stream);
+
+/*
+ * fp8q_int8_quant_rows -- int8 codes and one fp32 scale per row:
+ *   s = max_c |x| / 127 (IEEE fp32 division),  q = rint(RN_fp32(x / s)), ties
+ *   to even, saturated to [-127, 127];  s == 0 gives zeros.
+ *  x, x_dtype : FP8Q_F32 or FP8Q_BF16, row stride ldx >= cols.
+ *  q, ldq     : codes [rows][cols], q 16-byte aligned, ldq >= cols a multiple
+ *               of 16; s: fp32 [rows] (0 where cols == 0).
+ * Inputs must be finite; NaN or infinite inputs give unspecified codes.
+ */
+int fp8q_int8_quant_rows(const void* x, int x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                         int8_t* q, int64_t ldq, float* s, hipStream_t stream);
+
+/* Scratch bytes of fp8q_int8_gemm for these sizes (0: none needed). */
+int64_t fp8q_int8_gemm_workspace(int64_t M, int64_t N, int64_t K);
+
+/*
+ * fp8q_int8_gemm -- y = x W^T on int8 codes:
+ *   C[m][n] = (float)(sum_k A[m][k] * B[n][k]) * SA[m] * SB[n] + bias[n],
+ * the sum exact (int32), then each fp32 operation rounded once in this order,
+ * and once more for a bf16 output.
+ *  a, lda, sa : codes [M][K] and fp32 scales [M] (fp8q_int8_quant_rows).
+ *  b, ldb, sb : codes [N][K] and fp32 scales [N]: a weight's rows are its
+ *               output channels.
+ *  bias       : fp32 [N] or NULL.
+ *  c, ldc, c_dtype : output [M][N], FP8Q_F32 or FP8Q_BF16.
+ *  workspace  : at least fp8q_int8_gemm_workspace(M, N, K) bytes, 16-byte
+ *               aligned (NULL if that is 0).
+ * Alignment as fp8q.h: a, b, c 16-byte aligned, lda, ldb and ldc's bytes
+ * multiples of 16; what lies past column K of a row may hold anything.  K ==
+ * 0 gives the bias (or zeros); the operands and scales may then be NULL.
+ * K > 131071 (the sum could leave int32) and row strides of 2^23 or more are
+ * FP8Q_ERR_UNSUPPORTED.
+ */
+int fp8q_int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* sa,
+                   const int8_t* b, int64_t ldb, const float* sb, const float* bias,
+                   void* c, int64_t ldc, int c_dtype, void* workspace, int64_t workspace_bytes,
+                   hipStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FP8Q_OPS_H */
