@@ -5,6 +5,8 @@
 // fp32 exactly and rounded to nearest even once on the way out.
 #pragma once
 
+#include <type_traits>
+
 #include "fp8q_device.h"
 
 namespace fp8q {
@@ -98,19 +100,35 @@ __device__ __forceinline__ void store_row(T* row, int64_t c, int64_t cols, u32x4
     }
 }
 
-// Sum and maximum over the 64 lanes of a wave, in every lane (all active).
+// Sum and maximum over the 64 lanes of a wave, in every lane (all active):
+// four steps within the rows of 16 lanes as data-parallel moves, then the row
+// and half-wave swaps, each of which leaves a lane its own value and its
+// partner's (no trip through LDS; the tree is the same for every lane).
+template <typename Op>
+__device__ __forceinline__ float wave_reduce(float v, Op op)
+{
+    auto step = [&](auto ctrl) {
+        return op(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF,
+                                                                false)));
+    };
+    v = step(std::integral_constant<int, 0xB1>{});    // quad [1,0,3,2]
+    v = step(std::integral_constant<int, 0x4E>{});    // quad [2,3,0,1]
+    v = step(std::integral_constant<int, 0x141>{});   // half-row mirror
+    v = step(std::integral_constant<int, 0x140>{});   // row mirror
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return op(__uint_as_float(h[0]), __uint_as_float(h[1]));
+}
+
 __device__ __forceinline__ float wave_sum(float v)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    return v;
+    return wave_reduce(v, [](float a, float b) { return a + b; });
 }
 
 __device__ __forceinline__ float wave_max(float v)
 {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
+    return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
 }  // namespace fp8q

@@ -11,11 +11,12 @@ where the header says so.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import List, Optional, Sequence, Tuple
 
 import torch
 
-from . import (BF16, F32, TILE, Fp8qError, OK, _cdiv, _device, _dtype, _empty_aligned, _ld, _lib, _on, _ptr, _shape)
+from . import BF16, F32, TILE, Fp8qError, OK, _cdiv, _device, _dtype, _empty_aligned, _ld, _lib, _ptr, _shape
 
 STATE_F32, STATE_E4M3 = 0, 1
 
@@ -58,34 +59,57 @@ def _vector(name: str, t: Optional[torch.Tensor], n: int, dtype: torch.dtype) ->
                          (name, dtype, n, t.dtype, tuple(t.shape)))
 
 
+# the handle of a device's current stream without making a Stream object (1.8 us of a call less)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(index: int, **tensors: Optional[torch.Tensor]) -> None:
+    """Every tensor lies on the GPU the call runs on."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise ValueError("%s must be a torch.Tensor" % name)
+        if t.get_device() != index:
+            raise ValueError("%s is on %s, the call runs on cuda:%d" % (name, t.device, index))
+
+
+def _stride(t: torch.Tensor) -> int:
+    """Row stride of a 2-D tensor with unit column stride (the package's _ld, for the common case)."""
+    ld, one = t.stride()
+    rows, cols = t.shape
+    if one == 1:
+        return ld if rows > 1 else max(ld, cols)
+    return _ld(t)
+
+
 class _Call:
     """Where a call runs: its device and stream.  Memory allocated for the call belongs to the current stream;
     where the work goes to another one, the allocator is told (``keep``)."""
-    __slots__ = ("dev", "handle", "other", "guard")
+    __slots__ = ("dev", "handle", "other")
 
     def __init__(self, first: torch.Tensor, stream):
-        self.dev = first.device
         self.other = None
         if stream is None:
-            if self.dev.type != "cuda":
-                _device(first, stream)      # raises
-            self.handle = torch.cuda.current_stream(self.dev).cuda_stream
-        else:
-            self.dev = _device(first, stream)
-            self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-            if self.handle != torch.cuda.current_stream(self.dev).cuda_stream:
-                self.other = stream if isinstance(stream, torch.cuda.Stream) else \
-                    torch.cuda.ExternalStream(self.handle, device=self.dev)
-        # the library launches on the thread's current device
-        self.guard = None
-        if self.dev.index is not None and torch.cuda.current_device() != self.dev.index:
-            self.guard = torch.cuda.device(self.dev)
+            self.dev = first.get_device()
+            if self.dev < 0:
+                raise ValueError("operands must be GPU tensors, got a tensor on %s" % first.device)
+            self.handle = _raw_stream(self.dev)
+            return
+        dev = _device(first, stream)
+        self.dev = torch.cuda.current_device() if dev.index is None else dev.index
+        self.handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if self.handle != _raw_stream(self.dev):
+            self.other = stream if isinstance(stream, torch.cuda.Stream) else \
+                torch.cuda.ExternalStream(self.handle, device=torch.device("cuda", self.dev))
 
     def __call__(self, fn, where: str, *args) -> None:
-        if self.guard is None:
+        # (the library launches on the thread's current device)
+        if torch.cuda.current_device() == self.dev:
             st = fn(*args, self.handle)
         else:
-            with self.guard:
+            with torch.cuda.device(self.dev):
                 st = fn(*args, self.handle)
         if st != OK:
             raise Fp8qError(st, where)
@@ -95,6 +119,13 @@ class _Call:
             for t in tensors:
                 if t is not None:
                     t.record_stream(self.other)
+
+
+def _rows(rows: int, cols: int, dtype: torch.dtype, device: torch.device, align: int) -> torch.Tensor:
+    """A new [rows, cols] output, its row stride rounded up to `align` elements."""
+    if cols % align == 0 and cols:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    return _empty_aligned(rows, cols, dtype, device, align)
 
 
 # ---------------------------------------------------------------------------
@@ -118,19 +149,22 @@ def fp8q_layer_norm_forward(x: torch.Tensor, w: Optional[torch.Tensor] = None, b
     if wt is not None:
         _vector("w", w, cols, wt.dtype)
         _vector("b", b, cols, wt.dtype)
+    _on(call.dev, x=x, w=w, b=b, y=y, mean=mean, rstd=rstd)
     if y is None:
-        y = _empty_aligned(rows, cols, x.dtype, x.device, 8 if xd == BF16 else 4)
+        y = _rows(rows, cols, x.dtype, x.device, 8 if xd == BF16 else 4)
+    else:
+        _dtype("y", y, (x.dtype,))
+        _shape("y", y, (rows, cols))
     if mean is None:
         mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+    else:
+        _vector("mean", mean, rows, torch.float32)
     if rstd is None:
         rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _on(call.dev, x=x, w=w, b=b, y=y, mean=mean, rstd=rstd)
-    _dtype("y", y, (x.dtype,))
-    _shape("y", y, (rows, cols))
-    _vector("mean", mean, rows, torch.float32)
-    _vector("rstd", rstd, rows, torch.float32)
-    call(_lib.fp8q_layer_norm_forward, "fp8q_layer_norm_forward", x.data_ptr(), xd, rows, cols, _ld(x), _ptr(w),
-         _ptr(b), wd, eps, y.data_ptr(), _ld(y), mean.data_ptr(), rstd.data_ptr())
+    else:
+        _vector("rstd", rstd, rows, torch.float32)
+    call(_lib.fp8q_layer_norm_forward, "fp8q_layer_norm_forward", x.data_ptr(), xd, rows, cols, _stride(x), _ptr(w),
+         _ptr(b), wd, eps, y.data_ptr(), _stride(y), mean.data_ptr(), rstd.data_ptr())
     call.keep(y, mean, rstd)
     return y, mean, rstd
 
@@ -147,30 +181,31 @@ def fp8q_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tens
     xd = _float_code("x", x)
     wt = w if w is not None else dw if dw is not None else db
     wd = F32 if wt is None else _float_code("w", wt)
-    if dx is None:
-        dx = _empty_aligned(rows, cols, x.dtype, x.device, 8 if xd == BF16 else 4)
-    if w is not None:
-        if dw is None:
-            dw = torch.empty(cols, dtype=w.dtype, device=x.device)
-        if db is None:
-            db = torch.empty(cols, dtype=w.dtype, device=x.device)
     _on(call.dev, dy=dy, x=x, mean=mean, rstd=rstd, w=w, dx=dx, dw=dw, db=db)
     _dtype("dy", dy, (x.dtype,))
-    _dtype("dx", dx, (x.dtype,))
     _shape("dy", dy, (rows, cols))
-    _shape("dx", dx, (rows, cols))
     _vector("mean", mean, rows, torch.float32)
     _vector("rstd", rstd, rows, torch.float32)
     if wt is not None:
         _vector("w", w, cols, wt.dtype)
         _vector("dw", dw, cols, wt.dtype)
         _vector("db", db, cols, wt.dtype)
+    if dx is None:
+        dx = _rows(rows, cols, x.dtype, x.device, 8 if xd == BF16 else 4)
+    else:
+        _dtype("dx", dx, (x.dtype,))
+        _shape("dx", dx, (rows, cols))
+    if w is not None:
+        if dw is None:
+            dw = torch.empty(cols, dtype=w.dtype, device=x.device)
+        if db is None:
+            db = torch.empty(cols, dtype=w.dtype, device=x.device)
     ws, nws = None, 0
     if wt is not None:
         nws = _lib.fp8q_layer_norm_backward_workspace(rows, cols)
         ws = torch.empty(nws, dtype=torch.uint8, device=x.device)
-    call(_lib.fp8q_layer_norm_backward, "fp8q_layer_norm_backward", dy.data_ptr(), _ld(dy), x.data_ptr(), xd, rows,
-         cols, _ld(x), mean.data_ptr(), rstd.data_ptr(), _ptr(w), wd, dx.data_ptr(), _ld(dx), _ptr(dw), _ptr(db),
+    call(_lib.fp8q_layer_norm_backward, "fp8q_layer_norm_backward", dy.data_ptr(), _stride(dy), x.data_ptr(), xd, rows,
+         cols, _stride(x), mean.data_ptr(), rstd.data_ptr(), _ptr(w), wd, dx.data_ptr(), _stride(dx), _ptr(dw), _ptr(db),
          _ptr(ws), nws)
     call.keep(dx, dw, db, ws)
     return dx, dw, db
@@ -193,8 +228,9 @@ class AdamWPlan:
         if not params:
             raise ValueError("no parameters")
         dev = _device(params[0], None)
+        index = params[0].get_device()
         for i, p in enumerate(params):
-            _on(dev, **{"params[%d]" % i: p})
+            _on(index, **{"params[%d]" % i: p})
             if p.dtype != torch.float32 or not p.is_contiguous():
                 raise ValueError("params[%d] must be contiguous torch.float32, got %s" % (i, p.dtype))
         self.params: List[torch.Tensor] = params
@@ -212,7 +248,7 @@ class AdamWPlan:
         if len(moments) != len(want):
             raise ValueError("expected %d moment tensors, got %d" % (len(want), len(moments)))
         for i, (t, (dt, n)) in enumerate(zip(moments, want)):
-            _on(dev, **{"moments[%d]" % i: t})
+            _on(index, **{"moments[%d]" % i: t})
             _vector("moments[%d]" % i, t, n, dt)
         self.moments = moments
         self.device = dev
@@ -228,8 +264,7 @@ class AdamWPlan:
         self._table = self._host.to(dev)
         torch.cuda.current_stream(dev).synchronize()     # a step may run on any stream
         self._at = [p.data_ptr() for p in params]
-        self._p = (_p * count)(*self._at)
-        self._vectors = _p * count
+        self._p = array("Q", self._at)
 
 
 def fp8q_adamw_plan(params: Sequence[torch.Tensor], state_kind: int = STATE_E4M3, moments: Optional[tuple] = None
@@ -256,32 +291,34 @@ def fp8q_adamw_multi_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor
     if len(grads) != len(plan.sizes):
         raise ValueError("%d gradients for %d parameters" % (len(grads), len(plan.sizes)))
     call = _Call(plan.params[0], stream)
-    dev = plan.device
-    if [p.data_ptr() for p in plan.params] != plan._at:
+    tensor = torch.Tensor
+    if list(map(tensor.data_ptr, plan.params)) != plan._at:
         raise ValueError("a parameter has moved in memory since the plan was made")
-    gdtype, ptrs = None, []
-    for i, (g, n) in enumerate(zip(grads, plan.sizes)):
-        if g is None:
-            ptrs.append(None)
-            continue
-        if g.numel() != n or not g.is_contiguous() or g.device != dev:
-            raise ValueError("grads[%d] must be contiguous with %d elements on %s, got %s on %s" %
-                             (i, n, dev, tuple(g.shape), g.device))
-        if gdtype is None:
-            gdtype = g.dtype
-            gd = _float_code("grads[%d]" % i, g)
-        elif g.dtype != gdtype:
-            raise ValueError("gradients must have one type, got %s and %s" % (gdtype, g.dtype))
-        ptrs.append(g.data_ptr())
-    if gdtype is None:
-        return
+    live, sizes = grads, plan.sizes
+    if any(g is None for g in grads):
+        live = [g for g in grads if g is not None]
+        sizes = [n for g, n in zip(grads, sizes) if g is not None]
+        if not live:
+            return
+    # (checked list by list: a step over many small tensors is as long as this takes)
+    if list(map(tensor.numel, live)) != sizes or not all(map(tensor.is_contiguous, live)):
+        raise ValueError("grads must be contiguous with the parameters' numbers of elements")
+    index = plan.params[0].get_device()
+    if any(i != index for i in map(tensor.get_device, live)):
+        raise ValueError("grads must be on %s" % plan.device)
+    gdtypes = {g.dtype for g in live}
+    if len(gdtypes) > 1:
+        raise ValueError("grads must have one type, got %s" % ", ".join(sorted(map(str, gdtypes))))
+    gd = _float_code("grads", live[0])
+    ptrs = array("Q", map(tensor.data_ptr, live) if live is grads else
+                 [0 if g is None else g.data_ptr() for g in grads])
     if plan.kind == STATE_F32:
         m, v = plan.moments
         ms = vs = None
     else:
         m, ms, v, vs = plan.moments
-    call(_lib.fp8q_adamw_multi_step, "fp8q_adamw_multi_step", plan._host.data_ptr(), plan._table.data_ptr(), plan._p,
-         plan._vectors(*ptrs), gd, plan.kind, m.data_ptr(), _ptr(ms), v.data_ptr(), _ptr(vs), lr, beta1, beta2, eps,
+    call(_lib.fp8q_adamw_multi_step, "fp8q_adamw_multi_step", plan._host.data_ptr(), plan._table.data_ptr(), plan._p.buffer_info()[0],
+         ptrs.buffer_info()[0], gd, plan.kind, m.data_ptr(), _ptr(ms), v.data_ptr(), _ptr(vs), lr, beta1, beta2, eps,
          weight_decay, step)
     call.keep(plan._table)
 
@@ -297,16 +334,18 @@ def fp8q_int8_quant_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: O
     rows, cols = x.shape
     call = _Call(x, stream)
     xd = _float_code("x", x)
+    _on(call.dev, x=x, q=q, s=s)
     if q is None:
-        q = _empty_aligned(rows, cols, torch.int8, x.device, 16)
+        q = _rows(rows, cols, torch.int8, x.device, 16)
+    else:
+        _dtype("q", q, (torch.int8,))
+        _shape("q", q, (rows, cols))
     if s is None:
         s = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _on(call.dev, x=x, q=q, s=s)
-    _dtype("q", q, (torch.int8,))
-    _shape("q", q, (rows, cols))
-    _vector("s", s, rows, torch.float32)
-    call(_lib.fp8q_int8_quant_rows, "fp8q_int8_quant_rows", x.data_ptr(), xd, rows, cols, _ld(x), q.data_ptr(),
-         _ld(q), s.data_ptr())
+    else:
+        _vector("s", s, rows, torch.float32)
+    call(_lib.fp8q_int8_quant_rows, "fp8q_int8_quant_rows", x.data_ptr(), xd, rows, cols, _stride(x), q.data_ptr(),
+         _stride(q), s.data_ptr())
     call.keep(q, s)
     return q, s
 
@@ -321,21 +360,21 @@ def fp8q_int8_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
     if Kb != K:
         raise ValueError("contraction sizes differ: a %s, b %s" % (tuple(a.shape), tuple(b.shape)))
     call = _Call(a, stream)
-    if c is None:
-        if out_dtype not in _FLOATS:
-            raise ValueError("output dtype must be float32 or bfloat16")
-        c = _empty_aligned(M, N, out_dtype, a.device, 4 if out_dtype == torch.float32 else 8)
     _on(call.dev, a=a, sa=sa, b=b, sb=sb, bias=bias, c=c)
-    cd = _float_code("c", c)
     _dtype("a", a, (torch.int8,))
     _dtype("b", b, (torch.int8,))
     _vector("sa", sa, M, torch.float32)
     _vector("sb", sb, N, torch.float32)
     _vector("bias", bias, N, torch.float32)
+    if c is None:
+        if out_dtype not in _FLOATS:
+            raise ValueError("output dtype must be float32 or bfloat16")
+        c = _rows(M, N, out_dtype, a.device, 4 if out_dtype == torch.float32 else 8)
+    cd = _float_code("c", c)
     _shape("c", c, (M, N))
     nws = _lib.fp8q_int8_gemm_workspace(M, N, K)
     ws = torch.empty(nws, dtype=torch.uint8, device=a.device) if nws else None
-    call(_lib.fp8q_int8_gemm, "fp8q_int8_gemm", M, N, K, a.data_ptr(), _ld(a), sa.data_ptr(), b.data_ptr(), _ld(b),
-         sb.data_ptr(), _ptr(bias), c.data_ptr(), _ld(c), cd, _ptr(ws), nws)
+    call(_lib.fp8q_int8_gemm, "fp8q_int8_gemm", M, N, K, a.data_ptr(), _stride(a), sa.data_ptr(), b.data_ptr(), _stride(b),
+         sb.data_ptr(), _ptr(bias), c.data_ptr(), _stride(c), cd, _ptr(ws), nws)
     call.keep(c, ws)
     return c
