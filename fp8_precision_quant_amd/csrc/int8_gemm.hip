@@ -6,6 +6,8 @@
 // The sum is exact (int32; K <= 131071 keeps K * 128^2 below 2^31), so its
 // order and the way it is split never change the result; it is rounded to
 // fp32 once and each fp32 operation after it once, in the order above.
+#include <utility>
+
 #include "gemm_common.h"
 #include "gemm_lds.h"
 #include "ops_internal.h"
@@ -21,6 +23,18 @@ __device__ __forceinline__ float scaled(int acc, float sa, float sb, float bias)
     const float t = (float)acc * sa;
     const float u = t * sb;
     return u + bias;
+}
+
+// f(integral_constant 0), ..., f(integral_constant N - 1)
+template <int N, typename F, int... I>
+__device__ __forceinline__ void static_for_(F&& f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void static_for(F&& f)
+{
+    static_for_<N>(f, std::make_integer_sequence<int, N>{});
 }
 
 struct Int8Args {
@@ -161,121 +175,305 @@ __global__ __launch_bounds__(256) void int8_gemm_few_kernel(Int8Args p)
 }
 
 // ---------------------------------------------------------------------------
-// Tiles of 128 x BN, staged through LDS; K may be split over workgroups
+// Tiles staged through LDS; K may be split over workgroups
 // ---------------------------------------------------------------------------
 
-constexpr int kBM = 128;
 constexpr int kBK = 128;
 
-// Four waves, each 64 x BN / 2 of the tile.  Chunks of 128 along K travel from
-// memory to LDS directly, kDepth stages deep, with one barrier per chunk.
-// Rows past M or N and bytes past the operand's end read as zero (buffer
-// bounds); bytes between K and the next row's start are whatever lies there,
-// so the A rows of the last chunk are cleared from K on in LDS, which clears
-// the products.  With gridDim.y > 1 workgroup y takes its share of the chunks
-// and leaves int32 sums in ws[y][M][nstride] for int8_gemm_join_kernel.
-template <typename C, int BN, int DEPTH>
-__global__ __launch_bounds__(256) void int8_gemm_tile_kernel(Int8Args p, int tiles_n, int chunks_per, int64_t nstride)
+// s_waitcnt vmcnt(N): all of this wave's loads but the newest N have landed
+// (loads land in order; stores in between only make the wait stricter)
+template <int N>
+__device__ __forceinline__ void wait_loads()
 {
-    constexpr int NB = BN / 32;               // 16-column blocks per wave
-    constexpr int NA = kBM / 32, NL = BN / 32;   // loads of A and B per wave and chunk (8 rows each)
-    constexpr int kStage = (kBM + BN) * kBK;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[DEPTH * kStage];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t m0 = (int64_t)(blockIdx.x / tiles_n) * kBM, n0 = (int64_t)(blockIdx.x % tiles_n) * BN;
-    const int KB = (int)((p.K + kBK - 1) / kBK);
-    const int c0 = blockIdx.y * chunks_per, c1 = min(KB, c0 + chunks_per);
-    const int64_t k16 = (p.K + 15) & ~(int64_t)15;
-    const int64_t mrows = min(p.M - m0, (int64_t)kBM), nrows = min(p.N - n0, (int64_t)BN);
-    const __amdgpu_buffer_rsrc_t ra = rsrc(p.a + m0 * p.lda, (mrows - 1) * p.lda + k16);
-    const __amdgpu_buffer_rsrc_t rb = rsrc(p.b + n0 * p.ldb, (nrows - 1) * p.ldb + k16);
-    const uint32_t lds0 = lds_addr(smem);
-    const int lr = lane >> 3;
-    // load t of a wave fills LDS rows 8 (NA wave + t) .. + 7; the slot order within a row depends on the row
-    uint32_t va[NA], vb[NL];
+    static_assert(N >= 0 && N < 64, "vmcnt immediate");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// Slot order of B's 128-byte LDS rows in the large tile: chunk c (16 bytes) of
+// a row sits in slot c ^ bkey(row).  A fragment's 16 lanes read rows 8 a + b, a
+// and b below 4 (see the channel order below); with this key lanes 0-15, and
+// lanes 0-3, 12-15, 20-27, find their chunks in 16 different banks of 16 bytes.
+__device__ __forceinline__ int bkey(int row)
+{
+    const int a = (row >> 3) & 3;
+    return ((((a & 1) << 1) ^ (a & 2) ^ (a >> 1)) << 1) | ((row >> 1) & 1);     // 0, 2, 3, 1 from a
+}
+
+// 16 bytes of a buffer; what lies past its end reads as zero
+__device__ __forceinline__ v4f floats4(__amdgpu_buffer_rsrc_t rs, int64_t at)
+{
+    return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, (uint32_t)(4 * at), 0, 0));
+}
+
+// eight consecutive outputs, the first `left` of them inside the row
+template <typename C>
+__device__ __forceinline__ void store8(C* out, int64_t left, v4i lo, v4i hi, float sa, const v4f (&sb)[2],
+                                       const v4f (&bias)[2])
+{
+    float f[8];
 #pragma unroll
-    for (int t = 0; t < NA; ++t) {
-        const int r = 8 * (NA * wave + t) + lr;
+    for (int r = 0; r < 8; ++r) f[r] = scaled(r < 4 ? lo[r & 3] : hi[r & 3], sa, sb[r / 4][r & 3], bias[r / 4][r & 3]);
+    if (left >= 8) {
+        if constexpr (sizeof(C) == 2) {
+            *reinterpret_cast<uint4*>(out) = make_uint4(bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]),
+                                                        bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7]));
+        } else {
+            reinterpret_cast<float4*>(out)[0] = make_float4(f[0], f[1], f[2], f[3]);
+            reinterpret_cast<float4*>(out)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 7; ++r)
+            if (r < left) out[r] = narrow<C>(f[r]);
+    }
+}
+
+// acc += b a^T of a 16 x 64 block each.  In asm, so that the sums stay in
+// accumulation registers: with the builtin the compiler moved them about
+// between products where a wave holds 8 x 8 blocks (1.27 us a step for 0.5).
+__device__ __forceinline__ void product(v4i& acc, const v4i& b, const v4i& a)
+{
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
+
+// Four waves, each 16 NI x 16 NJ of a tile of 32 NI x 32 NJ.  K runs in chunks
+// of 128 (whole cache lines) of two steps, NI * NJ products each: while a
+// step's products are issued the fragments of the next step are read, one
+// read or load between products.  LDS holds the B of D chunks and the A of D +
+// 1: A of chunk c + D is loaded in the first step of chunk c, B in the second,
+// when this chunk's B is read out, with one barrier per chunk.  The loads run
+// on across the work items of a workgroup, an item being a tile and one of
+// `split` shares of its chunks.  A's bytes past K are cleared in LDS; what
+// follows K in a row of B then meets zeros.  Rows past M or N and bytes past
+// the operand's end read as zero (buffer bounds).
+// Block j of a wave's columns holds channels 32 (j / 2) + 8 (r / 4) + r % 4 +
+// 4 (j % 2), so a lane ends with eight consecutive channels of a token.
+template <typename C, int NI, int NJ, int D, int OCC>
+__global__ __launch_bounds__(256, OCC) void int8_gemm_tile_kernel(Int8Args p, int tiles_m, int tiles_n, int split,
+                                                                  int chunks_per, int64_t nstride)
+{
+    constexpr int BM = 32 * NI, BN = 32 * NJ;
+    constexpr int LA = NI, LB = NJ;                 // loads of A and B per wave and chunk (8 rows each)
+    constexpr uint32_t kA = BM * kBK, kB = BN * kBK, kRingA = (D + 1) * kA, kRingB = D * kB;
+    constexpr int GM = 8;                           // rows of tiles walked together
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[kRingA + kRingB];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // XCD x (workgroups x, x + 8, ...) owns a contiguous range of items, so its workgroups share panels in its L2
+    const int T = tiles_m * tiles_n, items = T * split, xcd = blockIdx.x & 7, local = blockIdx.x >> 3;
+    const int nwg = ((int)gridDim.x >> 3) + (xcd < (int)(gridDim.x & 7) ? 1 : 0);
+    const int first = xcd * (items >> 3) + min(xcd, items & 7), here = (items >> 3) + (xcd < (items & 7) ? 1 : 0);
+    if (local >= here) return;
+    const int my_items = (here - local + nwg - 1) / nwg;
+    const int KB = (int)((p.K + kBK - 1) / kBK);
+    const int tail = (int)(p.K % kBK);              // bytes of the last chunk that count, or 0: all
+    struct Item {
+        int64_t m0, n0;
+        int share, c0, c1;
+    };
+    auto item_at = [&](int ordinal) __attribute__((always_inline)) {
+        Item t;
+        const int id = first + local + ordinal * nwg, span = GM * tiles_n;
+        t.share = id / T;
+        const int pid = id - t.share * T, group = pid / span, idx = pid - group * span;
+        const int size = min(tiles_m - group * GM, GM);
+        t.m0 = (int64_t)(group * GM + idx % size) * BM;
+        t.n0 = (int64_t)(idx / size) * BN;
+        t.c0 = t.share * chunks_per;
+        t.c1 = min(KB, t.c0 + chunks_per);
+        return t;
+    };
+    const int64_t k16 = (p.K + 15) & ~(int64_t)15;
+    const uint32_t lds_a = lds_addr(smem), lds_b = lds_a + kRingA;
+
+    // the loader, D chunks ahead of the products
+    uint32_t va[LA], vb[LB];
+#pragma unroll
+    for (int t = 0; t < LA; ++t) {
+        const int r = 8 * (LA * wave + t) + (lane >> 3);
         va[t] = (uint32_t)(r * p.lda) + 16u * (uint32_t)((lane & 7) ^ swz_key(r));
     }
 #pragma unroll
-    for (int t = 0; t < NL; ++t) {
-        const int r = 8 * (NL * wave + t) + lr;
-        vb[t] = (uint32_t)(r * p.ldb) + 16u * (uint32_t)((lane & 7) ^ swz_key(r));
+    for (int t = 0; t < LB; ++t) {
+        const int r = 8 * (LB * wave + t) + (lane >> 3);
+        vb[t] = (uint32_t)(r * p.ldb) + 16u * (uint32_t)((lane & 7) ^ bkey(r));
     }
-    auto load = [&](int c, int st) __attribute__((always_inline)) {
-        // (past the last chunk: out of bounds, which reads nothing and keeps the count of loads)
-        const uint32_t k = c < c1 ? (uint32_t)c * kBK : 0x80000000u;
-        const uint32_t base = lds0 + (uint32_t)st * kStage;
-#pragma unroll
-        for (int t = 0; t < NA; ++t) dma16_at(ra, base + (uint32_t)(8 * (NA * wave + t) * kBK), va[t] + k, 0);
-#pragma unroll
-        for (int t = 0; t < NL; ++t) dma16_at(rb, base + (uint32_t)((kBM + 8 * (NL * wave + t)) * kBK), vb[t] + k, 0);
+    const __amdgpu_buffer_rsrc_t rsb = rsrc(p.sb, 4 * p.N), rbias = rsrc(p.bias, p.bias ? 4 * p.N : 0);
+    __amdgpu_buffer_rsrc_t ra, rb;
+    int lt = 0, lc, lc1;
+    uint32_t lk;
+    auto aim = [&]() __attribute__((always_inline)) {
+        const Item t = item_at(lt);
+        ra = rsrc(p.a + t.m0 * p.lda, (min(p.M - t.m0, (int64_t)BM) - 1) * p.lda + k16);
+        rb = rsrc(p.b + t.n0 * p.ldb, (min(p.N - t.n0, (int64_t)BN) - 1) * p.ldb + k16);
+        lc = t.c0;
+        lc1 = t.c1;
     };
-    for (int s = 0; s < DEPTH - 1; ++s) load(c0 + s, s);
-    const int wm = (wave >> 1) * 64, wn = (wave & 1) * (BN / 2);
+    aim();
+    lk = (uint32_t)lc * kBK;
+    auto advance = [&]() __attribute__((always_inline)) {
+        if (++lc == lc1 && ++lt < my_items) aim();
+        // (past the last item: out of bounds, which reads nothing and keeps the count of loads)
+        lk = lt < my_items ? (uint32_t)lc * kBK : 0x80000000u;
+    };
+    auto load_a = [&](int t, uint32_t buf) __attribute__((always_inline)) {
+        dma16_at(ra, buf + (uint32_t)(8 * (LA * wave + t) * kBK), va[t] + lk, 0);
+    };
+    auto load_b = [&](int t, uint32_t buf) __attribute__((always_inline)) {
+        dma16_at(rb, buf + (uint32_t)(8 * (LB * wave + t) * kBK), vb[t] + lk, 0);
+    };
+    // clears this wave's rows of an A buffer from byte `tail` on
+    auto clear = [&](uint32_t buf) __attribute__((always_inline)) {
+        uint8_t* const at = smem + (buf - lds_a);
+        for (int i = lane; i < 8 * LA * 8; i += 64) {
+            const int r = 8 * LA * wave + i / 8, chunk = i % 8;
+            if (16 * chunk + 16 > tail) {
+                uint4* const v = reinterpret_cast<uint4*>(at + sw(r, chunk));
+                *v = mask_bytes(*v, tail > 16 * chunk ? tail - 16 * chunk : 0);
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
+
     const int row = lane & 15, kg = lane >> 4;
-    v4i acc[4][NB] = {};
-    int st = 0;
-    for (int c = c0; c < c1; ++c) {
-        wait_vm<(DEPTH - 2) * (NA + NL)>();      // this wave's loads of chunk c have landed
-        uint8_t* const stage = smem + st * kStage;
-        if (c == KB - 1 && p.K % kBK) {
-            const int valid = (int)(p.K % kBK);
-            for (int i = lane; i < 8 * NA * 8; i += 64) {
-                const int r = 8 * NA * wave + i / 8, chunk = i % 8;
-                if (16 * chunk + 16 > valid) {
-                    uint4* const at = reinterpret_cast<uint4*>(stage + sw(r, chunk));
-                    *at = mask_bytes(*at, valid > 16 * chunk ? valid - 16 * chunk : 0);
+    const int wm = (wave >> 1) * 16 * NI, wn = (wave & 1) * 16 * NJ;
+    const int brow = wn + 8 * (row >> 2) + (row & 3);
+    uint32_t fa_at[2], fb_at[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        fa_at[h] = (uint32_t)sw(wm + row, 2 * kg + h);
+        fb_at[h] = (uint32_t)(brow * kBK + (((2 * kg + h) ^ bkey(brow)) << 4));
+    }
+    v4i fa[2][NI], fb[2][NJ], acc[NI][NJ];
+
+    // fragment t of step half H from the buffers a and b
+    auto read = [&](auto T_, auto H, uint32_t a, uint32_t b) __attribute__((always_inline)) {
+        constexpr int t = decltype(T_)::value, h = decltype(H)::value;
+        if constexpr (t < NJ) fb[h][t] = ds128<4096 * (t / 2) + 512 * (t % 2)>(b + fb_at[h]);
+        else fa[h][t - NJ] = ds128<2048 * (t - NJ)>(a + fa_at[h]);
+    };
+    // the fragments of half H are there (two a statement: every use comes after its statement)
+    auto arrived = [&](auto H) __attribute__((always_inline)) {
+        v4i (&x)[NI] = fa[decltype(H)::value];
+        v4i (&y)[NJ] = fb[decltype(H)::value];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < NI; i += 2) asm volatile("" : "+v"(x[i]), "+v"(x[i + 1])::"memory");
+#pragma unroll
+        for (int j = 0; j < NJ; j += 2) asm volatile("" : "+v"(y[j]), "+v"(y[j + 1])::"memory");
+    };
+    // the products of half H; the other half's fragments are read from a and b, `fill` is loaded
+    auto step = [&](auto H, uint32_t a, uint32_t b, uint32_t fill) __attribute__((always_inline)) {
+        constexpr int h = decltype(H)::value, loads = h == 0 ? LA : LB, reads = NI + NJ;
+        constexpr int spread = NI * NJ * 3 / 4;      // products between which reads and loads go
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_nop 1");                     // (moves of fragments by the compiler, before a matrix instruction reads them)
+        static_for<NI * NJ>([&](auto Q) __attribute__((always_inline)) {
+            constexpr int q = decltype(Q)::value, i = q / NJ, j = q % NJ;
+            product(acc[i][j], fb[h][j], fa[h][i]);
+            static_for<reads>([&](auto T_) __attribute__((always_inline)) {
+                if constexpr (decltype(T_)::value * spread / reads == q)
+                    read(T_, std::integral_constant<int, 1 - h>{}, a, b);
+            });
+            static_for<loads>([&](auto T_) __attribute__((always_inline)) {
+                constexpr int t = decltype(T_)::value;
+                if constexpr (t * spread / loads == q) {
+                    if constexpr (h == 0) load_a(t, fill);
+                    else load_b(t, fill);
                 }
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        }
-        __builtin_amdgcn_s_barrier();            // everyone's have, and chunk c - 1 has been read
-        const uint32_t base = lds0 + (uint32_t)(st * kStage);
-        v4i fa[4][2], fb[NB][2];
+            });
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        arrived(std::integral_constant<int, 1 - h>{});
+    };
+    // keeps moves into and out of the accumulators away from the matrix instructions (the compiler does not see those)
+    auto settle = [](v4i (&x)[NI][NJ]) __attribute__((always_inline)) {
+        asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) fa[i][h] = ds128<0>(base + (uint32_t)sw(wm + 16 * i + row, 2 * kg + h));
+            for (int j = 0; j < NJ; j += 2) asm volatile("s_nop 1" : "+a"(x[i][j]), "+a"(x[i][j + 1])::"memory");
+    };
+    const std::integral_constant<int, 0> half0;
+    const std::integral_constant<int, 1> half1;
+
 #pragma unroll
-            for (int j = 0; j < NB; ++j) fb[j][h] = ds128<0>(base + (uint32_t)(kBM * kBK + sw(wn + 16 * j + row, 2 * kg + h)));
-        }
-        load(c + DEPTH - 1, st == 0 ? DEPTH - 1 : st - 1);
-        asm volatile("s_waitcnt lgkmcnt(0)"
-                     : "+v"(fa[0][0]), "+v"(fa[1][0]), "+v"(fa[2][0]), "+v"(fa[3][0]), "+v"(fa[0][1]), "+v"(fa[1][1]),
-                       "+v"(fa[2][1]), "+v"(fa[3][1])
-                     :
-                     : "memory");
+    for (int c = 0; c < D; ++c) {
+        if (c) advance();
 #pragma unroll
-        for (int j = 0; j < NB; ++j) asm volatile("" : "+v"(fb[j][0]), "+v"(fb[j][1])::"memory");
+        for (int t = 0; t < LA; ++t) load_a(t, lds_a + c * kA);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[j][h], fa[i][h], acc[i][j], 0, 0, 0);
-        st = st == DEPTH - 1 ? 0 : st + 1;
+        for (int t = 0; t < LB; ++t) load_b(t, lds_b + c * kB);
     }
-    wait_vm<0>();      // no load may land after the workgroup has ended
+    Item it = item_at(0);
+    wait_loads<(D - 1) * (LA + LB)>();
+    if (tail && it.c0 == KB - 1) clear(lds_a);
+    __builtin_amdgcn_s_barrier();
+    static_for<NI + NJ>([&](auto T_) __attribute__((always_inline)) { read(T_, half0, lds_a, lds_b); });
+    arrived(half0);
+
+    uint32_t a = lds_a, b = lds_b;                  // the buffers of the chunk being multiplied
+    int landed = 0;
+    for (int o = 0; o < my_items; ++o) {
+        const Item next = item_at(o + 1 < my_items ? o + 1 : o);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + wm + 16 * i + row;
-        if (m >= p.M) continue;
-        if (gridDim.y > 1) {
-            int32_t* const w = p.ws + ((int64_t)blockIdx.y * p.M + m) * nstride;
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                const int64_t n = n0 + wn + 16 * j + 4 * kg;
-                if (n < p.N) *reinterpret_cast<v4i*>(w + n) = acc[i][j];     // (nstride is a multiple of 4)
-            }
+            for (int j = 0; j < NJ; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+        settle(acc);
+        for (int c = it.c0; c < it.c1; ++c) {
+            advance();
+            const uint32_t an = a + kA == lds_a + kRingA ? lds_a : a + kA;
+            const uint32_t bn = b + kB == lds_b + kRingB ? lds_b : b + kB;
+            // (the buffer before this chunk's: read out before the last barrier)
+            step(half0, a, b, a == lds_a ? lds_a + kRingA - kA : a - kA);
+            // The next chunk has landed; the first D - 1 of an item after an
+            // epilogue have by its wait, and its stores go on meanwhile.
+            if (c - it.c0 >= landed) wait_loads<(D - 1) * LA + (D - 2) * LB>();
+            if (tail && (c + 1 < it.c1 ? c + 1 : next.c0) == KB - 1) clear(an);
+            __builtin_amdgcn_s_barrier();                   // everyone's has, and this chunk's A and B are read out
+            step(half1, an, bn, b);
+            a = an;
+            b = bn;
+        }
+        settle(acc);
+        const int64_t m0 = it.m0 + wm + row, n0 = it.n0 + wn + 8 * kg;
+        if (NI * NJ < 64 && split > 1) {             // (the largest tile is not split: no registers for it)
+            int32_t* const w = p.ws + (it.share * p.M + m0) * nstride + n0;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j)         // (nstride is a multiple of 4)
+                    if (m0 + 16 * i < p.M && n0 + 32 * (j / 2) + 4 * (j % 2) < p.N)
+                        *reinterpret_cast<v4i*>(w + 16 * i * nstride + 32 * (j / 2) + 4 * (j % 2)) = acc[i][j];
         } else {
-            const float sa = p.sa[m];
+            float sa[NI];
+            v4f sb[NJ / 2][2], bias[NJ / 2][2];
 #pragma unroll
-            for (int j = 0; j < NB; ++j) store4<C>(p, m, n0 + wn + 16 * j + 4 * kg, acc[i][j], sa);
+            for (int i = 0; i < NI; ++i) sa[i] = p.sa[m0 + 16 * i < p.M ? m0 + 16 * i : p.M - 1];
+#pragma unroll
+            for (int j = 0; j < NJ / 2; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    sb[j][h] = floats4(rsb, n0 + 32 * j + 4 * h);
+                    bias[j][h] = floats4(rbias, n0 + 32 * j + 4 * h);
+                }
+            // (vmcnt(0), in the form the compiler counts: otherwise it waits for these loads in the next item's steps)
+            __builtin_amdgcn_s_waitcnt(0x0F70);
+            landed = D - 1;
+            C* const out = reinterpret_cast<C*>(p.c) + m0 * p.ldc + n0;
+            const bool whole = m0 - row + 16 * NI <= p.M && n0 - 8 * kg + 16 * NJ <= p.N;     // of the wave
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ / 2; ++j) {
+                    const int64_t left = whole ? 8 : m0 + 16 * i < p.M ? p.N - n0 - 32 * j : 0;
+                    if (left > 0)
+                        store8(out + 16 * i * p.ldc + 32 * j, left, acc[i][2 * j], acc[i][2 * j + 1], sa[i], sb[j], bias[j]);
+                }
         }
+        it = next;
     }
+    wait_loads<0>();      // no load may land after the workgroup has ended
 }
 
 // C from the split's sums: four columns a thread.
@@ -292,38 +490,112 @@ __global__ __launch_bounds__(256) void int8_gemm_join_kernel(Int8Args p, int spl
     }
 }
 
-// How a product is made, from its sizes alone.
+// ---------------------------------------------------------------------------
+// The choice of kernel, tile and split, from the sizes alone
+// ---------------------------------------------------------------------------
+
+// The tiles, with their measured times in us: `one` a chunk where a CU runs
+// one workgroup, `both` where it runs two, `end` an item's epilogue.  The
+// smaller tile is slower for its work (128 x 128 x 128 takes 0.50 us, 256 x
+// 256 x 128 takes 1.33) and fills the card where there are few.
+struct Tile {
+    int ni, nj, d, per_cu;
+    double one, both, end;
+};
+constexpr Tile kTiles[] = {
+    {8, 8, 2, 1, 1.33, 0, 10}, {4, 8, 3, 1, 0.86, 0, 5},       {4, 4, 4, 1, 0.50, 0, 2.5},
+    {4, 4, 2, 2, 0.62, 0.95, 5}, {2, 4, 3, 2, 0.36, 0.58, 2}, {2, 2, 4, 2, 0.23, 0.38, 1.5},
+};
+
+// CUs the choice counts with (the scratch size depends on sizes alone)
+constexpr int kPlanCus = 256;
+
+struct Int8Part {
+    int tile;            // index of kTiles
+    int split, chunks_per;
+    int64_t n;           // columns
+    double us;
+};
+
+// The fastest single launch by the table: the items are dealt in rounds of
+// one workgroup per place, a last round that half fills the card runs at
+// `one`; a split costs the join's launch and its traffic.
+Int8Part int8_part(int64_t M, int64_t N, int64_t K, bool may_split)
+{
+    const int cus = kPlanCus;
+    const int64_t KB = (K + kBK - 1) / kBK;
+    Int8Part best = {0, 1, (int)KB, N, 1e30};
+    for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+        const Tile& t = kTiles[i];
+        const int64_t tiles = ((M + 32 * t.ni - 1) / (32 * t.ni)) * ((N + 32 * t.nj - 1) / (32 * t.nj));
+        for (int split = 1; split <= 16; ++split) {
+            // (the largest tile is not split: 256 accumulators leave no registers for it)
+            if (split > 1 && (!may_split || t.ni * t.nj == 64 || split > KB / 2 || tiles * split > 2 * t.per_cu * cus)) break;
+            const int64_t per = (KB + split - 1) / split, shares = (KB + per - 1) / per;
+            if (shares != split) continue;
+            const int64_t items = tiles * split, room = (int64_t)t.per_cu * cus, full = items / room, rest = items % room;
+            const double whole = t.per_cu == 2 ? t.both : t.one;
+            double us = 4 + full * (per * whole + t.end);
+            if (rest > 0) us += per * (rest > cus ? whole : t.one) + t.end;
+            if (split > 1) us += 3.5 + (double)split * M * N * 8 / 3.5e6;
+            if (us < best.us) best = {i, split, (int)per, N, us};
+        }
+    }
+    return best;
+}
+
 struct Int8Plan {
     int few;             // blocks of 16 tokens of the few-token kernel, or 0
-    int bn, split, chunks_per;
-    int64_t nstride;
+    int parts;           // launches side by side along N
+    Int8Part part[2];
+    int64_t nstride;     // of the split's sums (a product in two parts is not split)
 };
 
 Int8Plan int8_plan(int64_t M, int64_t N, int64_t K)
 {
-    Int8Plan q = {0, 64, 1, 0, (N + 3) / 4 * 4};
-    if (M <= 32) {
+    Int8Plan q = {};
+    q.nstride = (N + 3) / 4 * 4;
+    // The few-token kernel reads all of A for 16 channels: it wins while that
+    // is little beside the weight, or the weight is small and latency counts
+    // (us, few against tiles: 1 x 14336 x 4096 15.6, 17.1; 16 tokens 19.7,
+    // 16.9; 32 tokens 27.8, 17.9; 32 x 4096 x 4096 8.6, 10.0).
+    if (M <= 8 || (M <= 32 && N * K <= 20000000)) {
         q.few = M <= 16 ? 1 : 2;
         return q;
     }
-    const int64_t KB = (K + kBK - 1) / kBK, tm = (M + kBM - 1) / kBM;
-    if (tm * ((N + 127) / 128) >= 512) q.bn = 128;
-    const int64_t tiles = tm * ((N + q.bn - 1) / q.bn);
-    int64_t split = tiles >= 256 ? 1 : 512 / tiles;
-    if (split > KB / 2) split = KB / 2;
-    if (split > 16) split = 16;
-    if (split < 1) split = 1;
-    q.chunks_per = (int)((KB + split - 1) / split);
-    q.split = (int)((KB + q.chunks_per - 1) / q.chunks_per);
+    const int cus = kPlanCus;
+    q.parts = 1;
+    q.part[0] = int8_part(M, N, K, true);
+    // Whole rounds of a large tile, then the remaining columns with whatever
+    // is fastest for them: 4096 x 14336 x 4096 is 3.5 rounds of 256 x 256.
+    const int64_t KB = (K + kBK - 1) / kBK;
+    double best = q.part[0].us;
+    for (int i = 0; i < 2; ++i) {
+        const Tile& t = kTiles[i];
+        const int64_t tm = (M + 32 * t.ni - 1) / (32 * t.ni), bn = 32 * t.nj, tn = (N + bn - 1) / bn;
+        const int64_t rounds = tm * tn / cus, cols = rounds * cus / tm;
+        if (cols == 0 || cols >= tn) continue;
+        const int64_t items = cols * tm, n = cols * bn;
+        const Int8Part first = {i, 1, (int)KB, n, 4 + (items + cus - 1) / cus * (KB * t.one + t.end)};
+        const Int8Part rest = int8_part(M, N - n, K, false);
+        if (first.us + rest.us < best) {
+            best = first.us + rest.us;
+            q.parts = 2;
+            q.part[0] = first;
+            q.part[1] = rest;
+        }
+    }
     return q;
 }
 
-template <typename C, int BN, int DEPTH>
-void launch_tile(const Int8Args& p, const Int8Plan& q, hipStream_t st)
+template <typename C, int I>
+void launch_tile(const Int8Args& p, const Int8Part& q, int64_t nstride, hipStream_t st)
 {
-    const int64_t tiles_n = (p.N + BN - 1) / BN, tiles = (p.M + kBM - 1) / kBM * tiles_n;
-    hipLaunchKernelGGL((int8_gemm_tile_kernel<C, BN, DEPTH>), dim3((uint32_t)tiles, (uint32_t)q.split), dim3(256),
-                       0, st, p, (int)tiles_n, q.chunks_per, q.nstride);
+    constexpr Tile t = kTiles[I];
+    const int64_t tm = (p.M + 32 * t.ni - 1) / (32 * t.ni), tn = (p.N + 32 * t.nj - 1) / (32 * t.nj);
+    const int64_t items = tm * tn * q.split, room = (int64_t)device_cu_count() * t.per_cu;
+    hipLaunchKernelGGL((int8_gemm_tile_kernel<C, t.ni, t.nj, t.d, t.per_cu>), dim3((uint32_t)(items < room ? items : room)),
+                       dim3(256), 0, st, p, (int)tm, (int)tn, q.split, q.chunks_per, nstride);
 }
 
 template <typename C>
@@ -342,12 +614,26 @@ void launch(const Int8Args& p, hipStream_t st)
         else hipLaunchKernelGGL((int8_gemm_few_kernel<C, 2>), grid, dim3(256), 0, st, p);
         return;
     }
-    if (q.bn == 128) launch_tile<C, 128, 2>(p, q, st);
-    else launch_tile<C, 64, 3>(p, q, st);
-    if (q.split > 1) {
+    Int8Args part = p;
+    for (int i = 0; i < q.parts; ++i) {
+        part.N = q.part[i].n;
+        switch (q.part[i].tile) {
+        case 0: launch_tile<C, 0>(part, q.part[i], q.nstride, st); break;
+        case 1: launch_tile<C, 1>(part, q.part[i], q.nstride, st); break;
+        case 2: launch_tile<C, 2>(part, q.part[i], q.nstride, st); break;
+        case 3: launch_tile<C, 3>(part, q.part[i], q.nstride, st); break;
+        case 4: launch_tile<C, 4>(part, q.part[i], q.nstride, st); break;
+        default: launch_tile<C, 5>(part, q.part[i], q.nstride, st); break;
+        }
+        part.b += part.N * p.ldb;
+        part.sb += part.N;
+        if (p.bias) part.bias += part.N;
+        part.c = reinterpret_cast<C*>(part.c) + part.N;
+    }
+    if (q.parts == 1 && q.part[0].split > 1) {
         const int64_t groups = (p.M * (q.nstride / 4) + 255) / 256;
         hipLaunchKernelGGL(int8_gemm_join_kernel<C>, dim3((uint32_t)(groups < 65536 ? groups : 65536)), dim3(256), 0,
-                           st, p, q.split, q.nstride);
+                           st, p, q.part[0].split, q.nstride);
     }
 }
 
@@ -356,7 +642,7 @@ void launch(const Int8Args& p, hipStream_t st)
 int64_t int8_gemm_workspace(int64_t M, int64_t N, int64_t K)
 {
     const Int8Plan q = int8_plan(M, N, K);
-    return q.split > 1 ? q.split * M * q.nstride * 4 : 0;
+    return q.parts == 1 && q.part[0].split > 1 ? q.part[0].split * M * q.nstride * 4 : 0;
 }
 
 void launch_int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* sa, const int8_t* b,

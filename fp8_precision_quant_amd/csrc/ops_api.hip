@@ -182,7 +182,7 @@ int fp8q_int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda
     if (lda < K || ldb < K || ldc < N || ldc > kMaxSize) return FP8Q_ERR_SHAPE;
     if (lda >= kMaxInt8Ld || ldb >= kMaxInt8Ld) return FP8Q_ERR_UNSUPPORTED;
     // (a launch's threads are counted in 32 bits)
-    if (cdiv(M, 64) * cdiv(N, 64) >= ((int64_t)1 << 23)) return FP8Q_ERR_UNSUPPORTED;
+    if (cdiv(M, 64) * cdiv(N, 64) >= ((int64_t)1 << 22)) return FP8Q_ERR_UNSUPPORTED;
     const int64_t need = fp8q::int8_gemm_workspace(M, N, K);
     if (need > 0 && !workspace) return FP8Q_ERR_NULL;
     if (need > 0 && workspace_bytes < need) return FP8Q_ERR_SHAPE;
