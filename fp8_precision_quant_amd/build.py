@@ -1,4 +1,5 @@
-"""Build libfp8q.so (the HIP kernels and the C ABI) for gfx950 with hipcc.
+"""Build libfp8q.so (the HIP kernels and the C ABI) for gfx950 with hipcc, and
+_fast.so (the native marshalling of operators.py) with the host compiler.
 
 Usage: ``python fp8_precision_quant_amd/build.py`` (run as a file: importing
 the package would first load the existing library), or ``__graft_entry__.build()``.
@@ -37,6 +38,31 @@ def _compile(src: str, obj: str) -> None:
         raise RuntimeError("hipcc failed on %s" % src)
 
 
+def _build_fast() -> str:
+    """_fast.so: host code against torch's headers, next to the library it calls."""
+    import sysconfig
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(HIPCC)))
+    if not os.path.exists(os.path.join(rocm, "include", "hip")):
+        rocm = "/opt/rocm"
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    out = os.path.join(HERE, "_fast.so")
+    tmp = out + ".tmp%d" % os.getpid()
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           *("-I" + p for p in (*include_paths(), sysconfig.get_paths()["include"], os.path.join(rocm, "include"))),
+           os.path.join(CSRC, "fast_calls.cpp"), "-o", tmp, "-L" + torch_lib, "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-L" + HERE, "-l:libfp8q.so", "-L" + os.path.join(rocm, "lib"), "-lamdhip64",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("the host compiler failed on fast_calls.cpp")
+    os.replace(tmp, out)
+    return out
+
+
 def build(verbose: bool = False) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -47,8 +73,9 @@ def build(verbose: bool = False) -> str:
     subprocess.check_call([HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", *objs,
                            "-o", tmp])
     os.replace(tmp, LIB)
+    fast = _build_fast()
     if verbose:
-        print("built", LIB)
+        print("built", LIB, fast)
     return LIB
 
 

@@ -1,0 +1,289 @@
+// The plain calls of operators.py, marshalled natively (CPython module
+// _fast).  A call of small tensors is as long as its host side: in Python the
+// checks, the outputs' allocation and the conversion of the arguments took 6
+// to 17 us of a call, its launch 4.
+//
+// Each function takes the arguments of the wrapper that calls it where nothing
+// is out of the ordinary (operands on the current device, outputs to be
+// allocated, the current stream) and returns
+//   the outputs, the work enqueued;
+//   an int: the status of the library's refusal;
+//   None: not such a call, or arguments that are refused.  Nothing was done,
+//   and the wrapper's own code makes the call or names the mistake.
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <hip/hip_runtime_api.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <vector>
+
+#include "../../include/fp8q_ops.h"
+
+namespace {
+
+PyObject* raw_stream = nullptr;     // device index -> handle of its current stream
+
+// An operand: an ordinary strided tensor on the GPU.
+const at::Tensor* operand(PyObject* o)
+{
+    if (!THPVariable_Check(o)) return nullptr;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.defined() || !t.is_cuda() || t.layout() != at::kStrided || t.unsafeGetTensorImpl()->is_python_dispatch())
+        return nullptr;
+    return &t;
+}
+
+int type_code(at::ScalarType t) { return t == at::kFloat ? FP8Q_F32 : t == at::kBFloat16 ? FP8Q_BF16 : -1; }
+
+// A matrix with unit column stride; its row stride in `ld`.
+bool matrix(const at::Tensor* t, int64_t* ld)
+{
+    if (!t || t->dim() != 2 || t->stride(1) != 1 || t->size(0) == 0 || t->size(1) == 0) return false;
+    *ld = t->size(0) > 1 ? t->stride(0) : std::max(t->stride(0), t->size(1));
+    return true;
+}
+
+bool vector(const at::Tensor* t, int64_t n, at::ScalarType type)
+{
+    return t && t->dim() == 1 && t->size(0) == n && t->scalar_type() == type && t->is_contiguous();
+}
+
+// The current device and its current stream, if `t` lies there.
+bool place(const at::Tensor& t, hipStream_t* stream, int* device)
+{
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) {
+        (void)hipGetLastError();
+        return false;
+    }
+    if (t.get_device() != dev) return false;
+    PyObject* index = PyLong_FromLong(dev);
+    PyObject* r = index ? PyObject_CallOneArg(raw_stream, index) : nullptr;
+    Py_XDECREF(index);
+    if (!r) {
+        PyErr_Clear();
+        return false;
+    }
+    *stream = static_cast<hipStream_t>(PyLong_AsVoidPtr(r));
+    Py_DECREF(r);
+    *device = dev;
+    return !PyErr_Occurred();
+}
+
+// A new [rows, cols] output whose row stride is a multiple of `align` elements.
+at::Tensor rows_out(const at::Tensor& like, int64_t rows, int64_t cols, at::ScalarType type, int64_t align)
+{
+    const int64_t ld = (cols + align - 1) / align * align;
+    at::Tensor t = at::empty({rows, ld}, like.options().dtype(type).requires_grad(false));
+    return ld == cols ? t : t.narrow(1, 0, cols);
+}
+
+at::Tensor floats(const at::Tensor& like, int64_t n)
+{
+    return at::empty({n}, like.options().dtype(at::kFloat).requires_grad(false));
+}
+
+PyObject* tuple_of(std::initializer_list<at::Tensor> ts)
+{
+    PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
+    Py_ssize_t i = 0;
+    for (const at::Tensor& t : ts) PyTuple_SET_ITEM(r, i++, THPVariable_Wrap(t));
+    return r;
+}
+
+#define PLAIN(cond) \
+    do { \
+        if (!(cond)) Py_RETURN_NONE; \
+    } while (0)
+
+// (x, w, b, eps) -> (y, mean, rstd)
+PyObject* layer_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    PLAIN(n == 4);
+    const at::Tensor* x = operand(a[0]);
+    int64_t ldx;
+    PLAIN(matrix(x, &ldx));
+    const int64_t rows = x->size(0), cols = x->size(1);
+    const int xd = type_code(x->scalar_type());
+    const at::Tensor* w = a[1] == Py_None ? nullptr : operand(a[1]);
+    const at::Tensor* b = a[2] == Py_None ? nullptr : operand(a[2]);
+    PLAIN(xd >= 0 && (w || a[1] == Py_None) && (b || a[2] == Py_None) && PyFloat_Check(a[3]));
+    const at::Tensor* wt = w ? w : b;
+    const int wd = wt ? type_code(wt->scalar_type()) : FP8Q_F32;
+    PLAIN(wd >= 0);
+    int dev;
+    hipStream_t st;
+    PLAIN(place(*x, &st, &dev));
+    PLAIN(!w || (vector(w, cols, wt->scalar_type()) && w->get_device() == dev));
+    PLAIN(!b || (vector(b, cols, wt->scalar_type()) && b->get_device() == dev));
+    at::Tensor y = rows_out(*x, rows, cols, x->scalar_type(), xd == FP8Q_BF16 ? 8 : 4);
+    at::Tensor mean = floats(*x, rows), rstd = floats(*x, rows);
+    const int s = fp8q_layer_norm_forward(x->data_ptr(), xd, rows, cols, ldx, w ? w->data_ptr() : nullptr,
+                                          b ? b->data_ptr() : nullptr, wd, PyFloat_AS_DOUBLE(a[3]), y.data_ptr(),
+                                          std::max(y.stride(0), cols), static_cast<float*>(mean.data_ptr()),
+                                          static_cast<float*>(rstd.data_ptr()), st);
+    if (s != FP8Q_OK) return PyLong_FromLong(s);
+    return tuple_of({y, mean, rstd});
+    END_HANDLE_TH_ERRORS
+}
+
+// (dy, x, mean, rstd, w) -> (dx, dw, db)
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    PLAIN(n == 5);
+    const at::Tensor *dy = operand(a[0]), *x = operand(a[1]), *mean = operand(a[2]), *rstd = operand(a[3]),
+                     *w = operand(a[4]);
+    int64_t lddy, ldx;
+    PLAIN(matrix(dy, &lddy) && matrix(x, &ldx) && w);
+    const int64_t rows = x->size(0), cols = x->size(1);
+    const int xd = type_code(x->scalar_type()), wd = type_code(w->scalar_type());
+    PLAIN(xd >= 0 && wd >= 0 && dy->scalar_type() == x->scalar_type() && dy->sizes() == x->sizes());
+    PLAIN(vector(mean, rows, at::kFloat) && vector(rstd, rows, at::kFloat) && vector(w, cols, w->scalar_type()));
+    int dev;
+    hipStream_t st;
+    PLAIN(place(*x, &st, &dev));
+    for (const at::Tensor* t : {dy, mean, rstd, w}) PLAIN(t->get_device() == dev);
+    at::Tensor dx = rows_out(*x, rows, cols, x->scalar_type(), xd == FP8Q_BF16 ? 8 : 4);
+    const at::TensorOptions wo = w->options().requires_grad(false);
+    at::Tensor dw = at::empty({cols}, wo), db = at::empty({cols}, wo);
+    const int64_t bytes = fp8q_layer_norm_backward_workspace(rows, cols);
+    at::Tensor ws = at::empty({bytes}, wo.dtype(at::kByte));
+    const int s = fp8q_layer_norm_backward(
+        dy->data_ptr(), lddy, x->data_ptr(), xd, rows, cols, ldx, static_cast<float*>(mean->data_ptr()),
+        static_cast<float*>(rstd->data_ptr()), w->data_ptr(), wd, dx.data_ptr(), std::max(dx.stride(0), cols),
+        dw.data_ptr(), db.data_ptr(), ws.data_ptr(), bytes, st);
+    if (s != FP8Q_OK) return PyLong_FromLong(s);
+    return tuple_of({dx, dw, db});
+    END_HANDLE_TH_ERRORS
+}
+
+// (x) -> (q, s)
+PyObject* int8_quant_rows(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    PLAIN(n == 1);
+    const at::Tensor* x = operand(a[0]);
+    int64_t ldx;
+    PLAIN(matrix(x, &ldx));
+    const int64_t rows = x->size(0), cols = x->size(1);
+    const int xd = type_code(x->scalar_type());
+    int dev;
+    hipStream_t st;
+    PLAIN(xd >= 0 && place(*x, &st, &dev));
+    at::Tensor q = rows_out(*x, rows, cols, at::kChar, 16), s = floats(*x, rows);
+    const int r = fp8q_int8_quant_rows(x->data_ptr(), xd, rows, cols, ldx, static_cast<int8_t*>(q.data_ptr()),
+                                       (cols + 15) / 16 * 16, static_cast<float*>(s.data_ptr()), st);
+    if (r != FP8Q_OK) return PyLong_FromLong(r);
+    return tuple_of({q, s});
+    END_HANDLE_TH_ERRORS
+}
+
+// (a, sa, b, sb, bias, out is bf16) -> c
+PyObject* int8_gemm(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    PLAIN(n == 6);
+    const at::Tensor *A = operand(a[0]), *sa = operand(a[1]), *B = operand(a[2]), *sb = operand(a[3]);
+    const at::Tensor* bias = a[4] == Py_None ? nullptr : operand(a[4]);
+    int64_t lda, ldb;
+    PLAIN(matrix(A, &lda) && matrix(B, &ldb) && (bias || a[4] == Py_None));
+    const int64_t M = A->size(0), N = B->size(0), K = A->size(1);
+    PLAIN(B->size(1) == K && A->scalar_type() == at::kChar && B->scalar_type() == at::kChar);
+    PLAIN(vector(sa, M, at::kFloat) && vector(sb, N, at::kFloat) && (!bias || vector(bias, N, at::kFloat)));
+    int dev;
+    hipStream_t st;
+    PLAIN(place(*A, &st, &dev));
+    for (const at::Tensor* t : {sa, B, sb}) PLAIN(t->get_device() == dev);
+    PLAIN(!bias || bias->get_device() == dev);
+    const bool bf16 = a[5] == Py_True;
+    at::Tensor c = rows_out(*A, M, N, bf16 ? at::kBFloat16 : at::kFloat, bf16 ? 8 : 4);
+    const int64_t bytes = fp8q_int8_gemm_workspace(M, N, K);
+    at::Tensor ws;
+    if (bytes) ws = at::empty({bytes}, A->options().dtype(at::kByte).requires_grad(false));
+    const int r = fp8q_int8_gemm(
+        M, N, K, static_cast<int8_t*>(A->data_ptr()), lda, static_cast<float*>(sa->data_ptr()),
+        static_cast<int8_t*>(B->data_ptr()), ldb, static_cast<float*>(sb->data_ptr()),
+        bias ? static_cast<float*>(bias->data_ptr()) : nullptr, c.data_ptr(), std::max(c.stride(0), N),
+        bf16 ? FP8Q_BF16 : FP8Q_F32, bytes ? ws.data_ptr() : nullptr, bytes, st);
+    if (r != FP8Q_OK) return PyLong_FromLong(r);
+    return THPVariable_Wrap(c);
+    END_HANDLE_TH_ERRORS
+}
+
+// (params, their addresses (buffer of uint64), sizes (buffer of int64), grads, table on the host, on the device,
+//  state kind, m, ms, v, vs, lr, beta1, beta2, eps, weight_decay, step) -> True
+PyObject* adamw_multi_step(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    PLAIN(n == 17 && PyList_CheckExact(a[0]) && (PyList_CheckExact(a[3]) || PyTuple_CheckExact(a[3])));
+    const Py_ssize_t count = PyList_GET_SIZE(a[0]);
+    PLAIN(PySequence_Fast_GET_SIZE(a[3]) == count && count > 0);
+    const auto* at0 = static_cast<const uint64_t*>(PyLong_AsVoidPtr(a[1]));
+    const auto* sizes = static_cast<const int64_t*>(PyLong_AsVoidPtr(a[2]));
+    PLAIN(at0 && sizes);
+    PyObject** grads = PySequence_Fast_ITEMS(a[3]);
+    const at::Tensor *host = THPVariable_Check(a[4]) ? &THPVariable_Unpack(a[4]) : nullptr, *dev_table = operand(a[5]);
+    PLAIN(host && dev_table && PyLong_Check(a[6]) && PyLong_Check(a[16]));
+    double h[5];
+    for (int i = 0; i < 5; ++i) {
+        PLAIN(PyFloat_Check(a[11 + i]));
+        h[i] = PyFloat_AS_DOUBLE(a[11 + i]);
+    }
+    float* moments[4];
+    for (int i = 0; i < 4; ++i) {
+        const at::Tensor* t = a[7 + i] == Py_None ? nullptr : operand(a[7 + i]);
+        PLAIN(t || a[7 + i] == Py_None);
+        moments[i] = t ? static_cast<float*>(t->data_ptr()) : nullptr;
+    }
+    int dev;
+    hipStream_t st;
+    PLAIN(place(*dev_table, &st, &dev));
+    std::vector<const void*> g((size_t)count);
+    int gd = -1;
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        const at::Tensor* p = operand(PyList_GET_ITEM(a[0], i));
+        PLAIN(p && (uint64_t)(uintptr_t)p->data_ptr() == at0[i]);
+        if (grads[i] == Py_None) continue;
+        const at::Tensor* t = operand(grads[i]);
+        PLAIN(t && t->numel() == sizes[i] && t->is_contiguous() && t->get_device() == dev);
+        const int d = type_code(t->scalar_type());
+        PLAIN(d >= 0 && (gd < 0 || gd == d));
+        gd = d;
+        g[(size_t)i] = t->data_ptr();
+    }
+    PLAIN(gd >= 0);
+    const long long step = PyLong_AsLongLong(a[16]);
+    const long kind = PyLong_AsLong(a[6]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+    const int s = fp8q_adamw_multi_step(host->data_ptr(), dev_table->data_ptr(), reinterpret_cast<float* const*>(at0), g.data(),
+                                        gd, (int)kind, moments[0], moments[1], moments[2], moments[3], h[0], h[1], h[2],
+                                        h[3], h[4], step, st);
+    if (s != FP8Q_OK) return PyLong_FromLong(s);
+    Py_RETURN_TRUE;
+    END_HANDLE_TH_ERRORS
+}
+
+PyObject* set_stream_getter(PyObject*, PyObject* f)
+{
+    Py_INCREF(f);
+    Py_XDECREF(raw_stream);
+    raw_stream = f;
+    Py_RETURN_NONE;
+}
+
+#define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(name)), METH_FASTCALL, nullptr}
+PyMethodDef methods[] = {FAST(layer_norm_forward), FAST(layer_norm_backward), FAST(int8_quant_rows), FAST(int8_gemm),
+                         FAST(adamw_multi_step), {"set_stream_getter", set_stream_getter, METH_O, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__fast() { return PyModule_Create(&module); }

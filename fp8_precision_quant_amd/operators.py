@@ -18,6 +18,11 @@ import torch
 
 from . import BF16, F32, TILE, Fp8qError, OK, _cdiv, _device, _dtype, _empty_aligned, _ld, _lib, _ptr, _shape
 
+try:
+    from . import _fast
+except ImportError as e:
+    raise ImportError("_fast.so is not built; run `python fp8_precision_quant_amd/build.py`") from e
+
 STATE_F32, STATE_E4M3 = 0, 1
 
 _i64, _int, _p, _d = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_double
@@ -62,6 +67,15 @@ def _vector(name: str, t: Optional[torch.Tensor], n: int, dtype: torch.dtype) ->
 # the handle of a device's current stream without making a Stream object (1.8 us of a call less)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+_fast.set_stream_getter(_raw_stream)
+
+
+def _done(result, where: str):
+    """What a native call (csrc/fast_calls.cpp) returned: the outputs, or the library's refusal."""
+    if type(result) is int:
+        raise Fp8qError(result, where)
+    return result
 
 
 def _on(index: int, **tensors: Optional[torch.Tensor]) -> None:
@@ -141,6 +155,10 @@ def fp8q_layer_norm_forward(x: torch.Tensor, w: Optional[torch.Tensor] = None, b
     ``w`` and ``b`` are vectors of ``cols`` elements, bf16 or fp32 and of one type; None stands for ones and zeros.
     ``y`` has x's type, its default row stride is rounded up to 16 bytes (as the quantizers read it); ``mean`` and
     ``rstd`` are fp32, as ``fp8q_layer_norm_backward`` takes them."""
+    if stream is None and y is None and mean is None and rstd is None:
+        r = _fast.layer_norm_forward(x, w, b, eps)
+        if r is not None:
+            return _done(r, "fp8q_layer_norm_forward")
     rows, cols = x.shape
     call = _Call(x, stream)
     xd = _float_code("x", x)
@@ -176,6 +194,10 @@ def fp8q_layer_norm_backward(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tens
     """Gradients of the layer norm: ``(dx, dw, db)`` from ``dy`` and the forward pass's ``x``, ``mean``, ``rstd`` and
     ``w``.  ``dx`` has x's type, ``dw`` and ``db`` have w's.  Without weights (``w`` None) dw and db are computed only
     where given (bf16 or fp32 vectors of one type), else returned as None."""
+    if stream is None and dx is None and dw is None and db is None and w is not None:
+        r = _fast.layer_norm_backward(dy, x, mean, rstd, w)
+        if r is not None:
+            return _done(r, "fp8q_layer_norm_backward")
     rows, cols = x.shape
     call = _Call(x, stream)
     xd = _float_code("x", x)
@@ -264,7 +286,8 @@ class AdamWPlan:
         self._table = self._host.to(dev)
         torch.cuda.current_stream(dev).synchronize()     # a step may run on any stream
         self._at = [p.data_ptr() for p in params]
-        self._p = array("Q", self._at)
+        self._p, self._n = array("Q", self._at), array("q", self.sizes)
+        self._at_address, self._sizes_address = self._p.buffer_info()[0], self._n.buffer_info()[0]
 
 
 def fp8q_adamw_plan(params: Sequence[torch.Tensor], state_kind: int = STATE_E4M3, moments: Optional[tuple] = None
@@ -290,6 +313,17 @@ def fp8q_adamw_multi_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor
         raise ValueError("plan must come from fp8q_adamw_plan")
     if len(grads) != len(plan.sizes):
         raise ValueError("%d gradients for %d parameters" % (len(grads), len(plan.sizes)))
+    if plan.kind == STATE_F32:
+        m, v = plan.moments
+        ms = vs = None
+    else:
+        m, ms, v, vs = plan.moments
+    if stream is None:
+        r = _fast.adamw_multi_step(plan.params, plan._at_address, plan._sizes_address, grads, plan._host, plan._table,
+                                   plan.kind, m, ms, v, vs, lr, beta1, beta2, eps, weight_decay, step)
+        if r is not None:
+            _done(r, "fp8q_adamw_multi_step")
+            return
     call = _Call(plan.params[0], stream)
     tensor = torch.Tensor
     if list(map(tensor.data_ptr, plan.params)) != plan._at:
@@ -312,12 +346,7 @@ def fp8q_adamw_multi_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor
     gd = _float_code("grads", live[0])
     ptrs = array("Q", map(tensor.data_ptr, live) if live is grads else
                  [0 if g is None else g.data_ptr() for g in grads])
-    if plan.kind == STATE_F32:
-        m, v = plan.moments
-        ms = vs = None
-    else:
-        m, ms, v, vs = plan.moments
-    call(_lib.fp8q_adamw_multi_step, "fp8q_adamw_multi_step", plan._host.data_ptr(), plan._table.data_ptr(), plan._p.buffer_info()[0],
+    call(_lib.fp8q_adamw_multi_step, "fp8q_adamw_multi_step", plan._host.data_ptr(), plan._table.data_ptr(), plan._at_address,
          ptrs.buffer_info()[0], gd, plan.kind, m.data_ptr(), _ptr(ms), v.data_ptr(), _ptr(vs), lr, beta1, beta2, eps,
          weight_decay, step)
     call.keep(plan._table)
@@ -331,6 +360,10 @@ def fp8q_int8_quant_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, s: O
                          stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """int8 codes ``q[rows, cols]`` (row stride a multiple of 16) and fp32 scales ``s[rows]`` of ``x`` (bf16 or
     fp32): s = max |x| / 127 of the row, q = rint(x / s)."""
+    if stream is None and q is None and s is None:
+        r = _fast.int8_quant_rows(x)
+        if r is not None:
+            return _done(r, "fp8q_int8_quant_rows")
     rows, cols = x.shape
     call = _Call(x, stream)
     xd = _float_code("x", x)
@@ -355,6 +388,10 @@ def fp8q_int8_gemm(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch
                    c: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """``C[M, N] = (a b^T) * sa[:, None] * sb[None, :] + bias`` of int8 codes ``a[M, K]`` and ``b[N, K]`` with fp32
     scales ``sa[M]`` (tokens) and ``sb[N]`` (output channels) and an fp32 ``bias[N]``; bf16 or fp32 out."""
+    if stream is None and c is None and (out_dtype is torch.bfloat16 or out_dtype is torch.float32):
+        r = _fast.int8_gemm(a, sa, b, sb, bias, out_dtype is torch.bfloat16)
+        if r is not None:
+            return _done(r, "fp8q_int8_gemm")
     M, K = a.shape
     N, Kb = b.shape
     if Kb != K:
