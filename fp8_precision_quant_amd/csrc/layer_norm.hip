@@ -224,7 +224,11 @@ __global__ __launch_bounds__(kThreads) void ln_fwd_kernel(const T* __restrict__ 
     }
 }
 
-// dx of a row and its part of dw and db, one pass over x and dy.  As in the
+// dx of a row and its part of dw and db, one pass over x and dy: 4096 x 4096
+// bf16 27 us with the join (3.7 TB/s), 16384 x 4096 86 us (4.7).  Bound by
+// memory and, at one workgroup per CU, by its arithmetic: keeping u and xh
+// between the sums and dx, and the repeats' selects out of the common path,
+// took 31 to 27 us; four rows at a time instead gained nothing.  As in the
 // forward pass a row lies in the registers of TPR threads and a workgroup (or
 // each wave of one, TPR = 64) walks rows with the next one's loads under way.
 // A thread keeps its columns' sums of dy xh and dy over all its rows and
@@ -275,21 +279,33 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_bwd_row_kernel(
         for (int k = 0; k < NV; ++k) xc[k] = xr[k], gc[k] = gr[k];
         const float cmu = mu, crs = rs;
         if (AHEAD && r + stride < rows) load(r + stride);
-        float s1 = 0.0f, s2 = 0.0f;
+        float s1 = 0.0f, s2 = 0.0f, xh[NV][K], u[NV][K];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            float xv[K], gv[K], t1 = 0.0f, t2 = 0.0f;
-            unpack<T>(xc[k], xv);
-            unpack<T>(gc[k], gv);
+            float t1 = 0.0f, t2 = 0.0f;
+            unpack<T>(xc[k], xh[k]);
+            unpack<T>(gc[k], u[k]);
             if constexpr (!KEEP) load_weights<T>(w, w_bf16, 1.0f, sl[k].c, wv[k]);
 #pragma unroll
             for (int i = 0; i < K; ++i) {
-                const float xh = (xv[i] - cmu) * crs;
-                aw[k][i] += gv[i] * xh;
-                ab[k][i] += gv[i];
-                const float u = i >= sl[k].dup ? gv[i] * wv[k][i] : 0.0f;
-                t1 += u;
-                t2 += i >= sl[k].dup ? u * xh : 0.0f;
+                xh[k][i] = (xh[k][i] - cmu) * crs;
+                aw[k][i] = __builtin_fmaf(u[k][i], xh[k][i], aw[k][i]);
+                ab[k][i] += u[k][i];
+                u[k][i] *= wv[k][i];
+            }
+            // (the one vector that repeats elements of another leaves them out of the sums)
+            if (sl[k].dup == 0) {
+#pragma unroll
+                for (int i = 0; i < K; ++i) {
+                    t1 += u[k][i];
+                    t2 = __builtin_fmaf(u[k][i], xh[k][i], t2);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < K; ++i) {
+                    t1 += i >= sl[k].dup ? u[k][i] : 0.0f;
+                    t2 += i >= sl[k].dup ? u[k][i] * xh[k][i] : 0.0f;
+                }
             }
             s1 += t1;
             s2 += t2;
@@ -313,17 +329,13 @@ __global__ __launch_bounds__(TPR > 256 ? TPR : 256) void ln_bwd_row_kernel(
             parity ^= 1;
         }
         if (!dx) continue;
-        const float c1 = s1 / n, c2 = s2 / n;
+        const float c1 = -s1 / n * crs, c2 = -s2 / n * crs;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (sl[k].dup >= K) continue;
-            float xv[K], gv[K];
-            unpack<T>(xc[k], xv);
-            unpack<T>(gc[k], gv);
-            if constexpr (!KEEP) load_weights<T>(w, w_bf16, 1.0f, sl[k].c, wv[k]);
 #pragma unroll
-            for (int i = 0; i < K; ++i) xv[i] = crs * (gv[i] * wv[k][i] - c1 - (xv[i] - cmu) * crs * c2);
-            store16(dx + r * lddx + sl[k].c, pack<T>(xv));
+            for (int i = 0; i < K; ++i) u[k][i] = __builtin_fmaf(u[k][i], crs, __builtin_fmaf(xh[k][i], c2, c1));
+            store16(dx + r * lddx + sl[k].c, pack<T>(u[k]));
         }
     }
     if (!part) return;
@@ -398,49 +410,66 @@ __global__ __launch_bounds__(kThreads) void ln_bwd_cols_kernel(const T* __restri
                                                                const float* __restrict__ rstd,
                                                                float* __restrict__ part)
 {
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= cols) return;
-    float sw = 0.0f, sb = 0.0f;
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
-        const float g = widen(dy[r * lddy + c]);
-        sw += g * ((widen(x[r * ldx + c]) - mean[r]) * rstd[r]);
-        sb += g;
+    for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < cols; c += (int64_t)gridDim.x * kThreads) {
+        float sw = 0.0f, sb = 0.0f;
+        for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+            const float g = widen(dy[r * lddy + c]);
+            sw += g * ((widen(x[r * ldx + c]) - mean[r]) * rstd[r]);
+            sb += g;
+        }
+        part[((int64_t)blockIdx.y * 2) * cols + c] = sw;
+        part[((int64_t)blockIdx.y * 2 + 1) * cols + c] = sb;
     }
-    part[((int64_t)blockIdx.y * 2) * cols + c] = sw;
-    part[((int64_t)blockIdx.y * 2 + 1) * cols + c] = sb;
 }
 
-// dw (blockIdx.y 0) and db (1): 64 columns per workgroup, its 16 waves each
-// adding every 16th part.
+// dw (blockIdx.y 0) and db (1), 64 columns at a time: 64 groups of 16 lanes
+// each add every 64th part, four columns a lane with their loads in flight
+// together, then meet across the wave's four groups and in LDS.
 template <typename W>
 __global__ __launch_bounds__(1024) void ln_bwd_join_kernel(const float* __restrict__ part, int64_t parts, int64_t cols,
                                                            W* __restrict__ dw, W* __restrict__ db)
 {
     __shared__ float sum[16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, group = threadIdx.x >> 4;
     W* const out = blockIdx.y ? db : dw;
     if (!out) return;
-    float s = 0.0f;
-    if (c < cols)
-        for (int64_t q = wave; q < parts; q += 16) s += part[(2 * q + blockIdx.y) * cols + c];
-    sum[wave][lane] = s;
-    __syncthreads();
-    if (wave == 0 && c < cols) {
-        float t[16];
+    for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < cols; c0 += (int64_t)gridDim.x * 64) {
+        const int64_t c = c0 + 4 * (lane & 15);
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int64_t q = group; q < parts; q += 64) {
+            float v[4];
+            unpack<float>(load_row(part + (2 * q + blockIdx.y) * cols, c, cols), v);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) t[k] = sum[k][lane];
+            for (int i = 0; i < 4; ++i) s[i] += v[i];
+        }
 #pragma unroll
-        for (int d = 8; d > 0; d /= 2)
+        for (int i = 0; i < 4; ++i) {
+            s[i] += __shfl_xor(s[i], 16);
+            s[i] += __shfl_xor(s[i], 32);
+        }
+        __syncthreads();   // the previous columns' reads are over
+        if (lane < 16)
 #pragma unroll
-            for (int k = 0; k < d; ++k) t[k] += t[k + d];
-        out[c] = narrow<W>(t[0]);
+            for (int i = 0; i < 4; ++i) sum[wave][4 * lane + i] = s[i];
+        __syncthreads();
+        if (wave == 0 && c0 + lane < cols) {
+            float t[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) t[k] = sum[k][lane];
+#pragma unroll
+            for (int d = 8; d > 0; d /= 2)
+#pragma unroll
+                for (int k = 0; k < d; ++k) t[k] += t[k + d];
+            out[c0 + lane] = narrow<W>(t[0]);
+        }
     }
 }
 
 // Parts of the column sums: workgroups that each walk some of the rows.  One
-// per CU keeps the join small and is enough to stream: on 4096 x 4096 bf16 30
-// us with 256, 33 with 512, 46 with 1024.
+// per CU keeps the join small and is enough to stream (256, against 512: 4096
+// x 4096 bf16 27.3, 27.6 us; 1000 x 2047 fp32 12.4, 15.3; 4096 x 8192 bf16
+// 44.7, 51.2; only 16384 x 4096 gains, 86.1, 83.7).
 constexpr int64_t kMaxParts = 256;
 int64_t row_parts(int64_t rows) { return rows < kMaxParts ? (rows < 1 ? 1 : rows) : kMaxParts; }
 
@@ -496,7 +525,9 @@ int64_t backward_rows(const void* dy, int64_t lddy, const void* x, int64_t rows,
     constexpr int threads = TPR > 256 ? TPR : 256;
     constexpr int rpg = TPR == 64 ? 4 : 1;
     const int64_t groups = (rows + rpg - 1) / rpg;
-    const int64_t grid = groups < kMaxParts ? groups : kMaxParts;
+    // (two turns a workgroup, half the parts to join, where there are rows for
+    // it: 300 x 4096 bf16 12.3 -> 10.7 us; 20 rows 6.4 with one turn, 7.0 with two)
+    const int64_t turns = groups > 64 ? (groups + 1) / 2 : groups, grid = turns < kMaxParts ? turns : kMaxParts;
     hipLaunchKernelGGL((ln_bwd_row_kernel<T, TPR, NV>), dim3((uint32_t)grid), dim3(threads), 0, st, (const T*)dy, lddy,
                        (const T*)x, rows, cols, ldx, mean, rstd, w, w_dtype == FP8Q_BF16, (T*)dx, lddx, part);
     return grid;
@@ -505,8 +536,9 @@ int64_t backward_rows(const void* dy, int64_t lddy, const void* x, int64_t rows,
 template <typename W>
 void backward_join(const float* part, int64_t parts, int64_t cols, void* dw, void* db, hipStream_t st)
 {
-    hipLaunchKernelGGL((ln_bwd_join_kernel<W>), dim3((uint32_t)((cols + 63) / 64), 2), dim3(1024), 0, st, part, parts,
-                       cols, (W*)dw, (W*)db);
+    const int64_t groups = (cols + 63) / 64;
+    hipLaunchKernelGGL((ln_bwd_join_kernel<W>), dim3((uint32_t)(groups < 65536 ? groups : 65536), 2), dim3(1024), 0, st,
+                       part, parts, cols, (W*)dw, (W*)db);
 }
 
 template <typename T>
@@ -538,7 +570,8 @@ void backward(const void* dy, int64_t lddy, const void* x, int64_t rows, int64_t
         }
         if (part) {
             parts = row_parts(rows);
-            const dim3 cgrid((uint32_t)((cols + kThreads - 1) / kThreads), (uint32_t)parts);
+            const int64_t cgroups = (cols + kThreads - 1) / kThreads;
+            const dim3 cgrid((uint32_t)(cgroups < 65536 ? cgroups : 65536), (uint32_t)parts);
             hipLaunchKernelGGL((ln_bwd_cols_kernel<T>), cgrid, dim3(kThreads), 0, st, (const T*)dy, lddy, (const T*)x,
                                rows, cols, ldx, mean, rstd, part);
         }
