@@ -503,8 +503,8 @@ struct Tile {
     double one, both, end;
 };
 constexpr Tile kTiles[] = {
-    {8, 8, 2, 1, 1.33, 0, 10}, {4, 8, 3, 1, 0.86, 0, 5},       {4, 4, 4, 1, 0.50, 0, 2.5},
-    {4, 4, 2, 2, 0.62, 0.95, 5}, {2, 4, 3, 2, 0.36, 0.58, 2}, {2, 2, 4, 2, 0.23, 0.38, 1.5},
+    {8, 8, 2, 1, 1.33, 0, 10},   {4, 8, 3, 1, 0.86, 0, 5},     {4, 4, 4, 1, 0.50, 0, 2.5},
+    {2, 4, 3, 2, 0.36, 0.58, 2}, {2, 2, 4, 2, 0.23, 0.38, 1.5},
 };
 
 // CUs the choice counts with (the scratch size depends on sizes alone)
@@ -622,8 +622,7 @@ void launch(const Int8Args& p, hipStream_t st)
         case 1: launch_tile<C, 1>(part, q.part[i], q.nstride, st); break;
         case 2: launch_tile<C, 2>(part, q.part[i], q.nstride, st); break;
         case 3: launch_tile<C, 3>(part, q.part[i], q.nstride, st); break;
-        case 4: launch_tile<C, 4>(part, q.part[i], q.nstride, st); break;
-        default: launch_tile<C, 5>(part, q.part[i], q.nstride, st); break;
+        default: launch_tile<C, 4>(part, q.part[i], q.nstride, st); break;
         }
         part.b += part.N * p.ldb;
         part.sb += part.N;
