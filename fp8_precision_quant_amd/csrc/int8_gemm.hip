@@ -104,17 +104,20 @@ __device__ __forceinline__ v4i row16(const int8_t* row, int64_t k, int64_t K)
     return v4i{(int)v.x, (int)v.y, (int)v.z, (int)v.w};
 }
 
-// One workgroup makes MB blocks of 16 tokens times 16 output channels; its
-// four waves take every fourth 128 bytes of K and meet in LDS at the end, so
+// One workgroup makes MB blocks of 16 tokens times 16 output channels; its W
+// waves take every W-th 128 bytes of K and meet in LDS at the end, so
 // the weight streams through 64-lane loads with U of them in flight, no LDS
 // on the way, and nothing is left to join.  Lane l feeds row l % 16 of both
 // operands: bytes 32 (l / 16) .. + 31 of the 128, two matrix instructions (any
-// pairing of k with lanes will do that is the same for A and B).
-template <typename C, int MB>
-__global__ __launch_bounds__(256) void int8_gemm_few_kernel(Int8Args p)
+// pairing of k with lanes will do that is the same for A and B).  Bound by the
+// weight's bytes: 1 x 14336 x 4096 14.3 us (4.1 TB/s; a copy reaches 5.1), 1 x
+// 4096 x 14336 13.6; non-temporal loads of the weight were no faster (15.8).
+template <typename C, int MB, int W>
+__global__ __launch_bounds__(64 * W) void int8_gemm_few_kernel(Int8Args p)
 {
-    constexpr int U = 4;     // 128-byte steps in flight
-    __shared__ v4i part[3][MB][64];
+    constexpr int U = W == 16 && MB == 2 ? 2 : 4;     // 128-byte steps in flight (16 waves: 128 registers)
+    constexpr int kStride = 128 * W;
+    __shared__ v4i part[W - 1][MB][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, kg = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
@@ -133,11 +136,11 @@ __global__ __launch_bounds__(256) void int8_gemm_few_kernel(Int8Args p)
             acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b1, a1[i], acc[i], 0, 0, 0);
         }
     };
-    for (; k + (U - 1) * 512 < whole; k += U * 512) {
+    for (; k + (U - 1) * kStride < whole; k += U * kStride) {
         v4i b0[U], b1[U], a0[U][MB], a1[U][MB];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t at = k + u * 512 + 32 * kg;
+            const int64_t at = k + u * kStride + 32 * kg;
             b0[u] = *reinterpret_cast<const v4i*>(b + at);
             b1[u] = *reinterpret_cast<const v4i*>(b + at + 16);
 #pragma unroll
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(256) void int8_gemm_few_kernel(Int8Args p)
 #pragma unroll
         for (int u = 0; u < U; ++u) step(b0[u], b1[u], a0[u], a1[u]);
     }
-    for (; k < p.K; k += 512) {
+    for (; k < p.K; k += kStride) {
         const int64_t at = k + 32 * kg;
         const v4i b0 = row16(b, at, p.K), b1 = row16(b, at + 16, p.K);
         v4i a0[MB], a1[MB];
@@ -169,7 +172,9 @@ __global__ __launch_bounds__(256) void int8_gemm_few_kernel(Int8Args p)
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
         const int64_t m = 16 * i + row;
-        const v4i t = acc[i] + part[0][i][lane] + part[1][i][lane] + part[2][i][lane];
+        v4i t = acc[i];
+#pragma unroll
+        for (int v = 0; v < W - 1; ++v) t += part[v][i][lane];
         if (m < p.M) store4<C>(p, m, n0 + 4 * kg, t, p.sa[m]);
     }
 }
@@ -248,6 +253,12 @@ __device__ __forceinline__ void product(v4i& acc, const v4i& b, const v4i& a)
 // the operand's end read as zero (buffer bounds).
 // Block j of a wave's columns holds channels 32 (j / 2) + 8 (r / 4) + r % 4 +
 // 4 (j % 2), so a lane ends with eight consecutive channels of a token.
+// Bound, in the largest tile, by the matrix cores at the clock that their power
+// leaves: 8192 x 8192 x 8192 in 380 us (2890 TOP/s), whatever the places of
+// reads and loads among the products (375 to 391 us over seven schedules);
+// 4096 x 14336 x 4096 in 190 us, 117 MB of output among it.  The small tiles
+// are bound by the latency of a step, 0.12 us.  Chunks of 64 (half a cache
+// line a row) took twice the lines from L2: 632 us for 8192 x 8192 x 8192.
 template <typename C, int NI, int NJ, int D, int OCC>
 __global__ __launch_bounds__(256, OCC) void int8_gemm_tile_kernel(Int8Args p, int tiles_m, int tiles_n, int split,
                                                                   int chunks_per, int64_t nstride)
@@ -598,6 +609,14 @@ void launch_tile(const Int8Args& p, const Int8Part& q, int64_t nstride, hipStrea
                        dim3(256), 0, st, p, (int)tm, (int)tn, q.split, q.chunks_per, nstride);
 }
 
+template <typename C, int W>
+void launch_few(const Int8Args& p, int blocks, hipStream_t st)
+{
+    const dim3 grid((uint32_t)((p.N + 15) / 16));
+    if (blocks == 1) hipLaunchKernelGGL((int8_gemm_few_kernel<C, 1, W>), grid, dim3(64 * W), 0, st, p);
+    else hipLaunchKernelGGL((int8_gemm_few_kernel<C, 2, W>), grid, dim3(64 * W), 0, st, p);
+}
+
 template <typename C>
 void launch(const Int8Args& p, hipStream_t st)
 {
@@ -609,9 +628,11 @@ void launch(const Int8Args& p, hipStream_t st)
     }
     const Int8Plan q = int8_plan(p.M, p.N, p.K);
     if (q.few) {
-        const dim3 grid((uint32_t)((p.N + 15) / 16));
-        if (q.few == 1) hipLaunchKernelGGL((int8_gemm_few_kernel<C, 1>), grid, dim3(256), 0, st, p);
-        else hipLaunchKernelGGL((int8_gemm_few_kernel<C, 2>), grid, dim3(256), 0, st, p);
+        // Eight waves a workgroup, sixteen where there is at most one a CU and
+        // K is long (us, 4, 8 and 16 waves: 1 x 14336 x 4096 14.7, 14.3, 16.7;
+        // 1 x 4096 x 14336 16.6, 15.3, 13.6; 1 x 14336 x 1024 6.1, 5.9, 8.3).
+        if (p.N <= 16 * kPlanCus && p.K > 8192) launch_few<C, 16>(p, q.few, st);
+        else launch_few<C, 8>(p, q.few, st);
         return;
     }
     Int8Args part = p;

@@ -130,8 +130,8 @@ int64_t fp8q_int8_gemm_workspace(int64_t M, int64_t N, int64_t K);
  * Alignment as fp8q.h: a, b, c 16-byte aligned, lda, ldb and ldc's bytes
  * multiples of 16; what lies past column K of a row may hold anything.  K ==
  * 0 gives the bias (or zeros); the operands and scales may then be NULL.
- * K > 131071 (the sum could leave int32) and row strides of 2^23 or more are
- * FP8Q_ERR_UNSUPPORTED.
+ * K > 131071 (the sum could leave int32), row strides of 2^23 or more, N of
+ * 2^26 or more and outputs of 2^34 elements or more are FP8Q_ERR_UNSUPPORTED.
  */
 int fp8q_int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* sa,
                    const int8_t* b, int64_t ldb, const float* sb, const float* bias,

@@ -16,11 +16,12 @@ bf16, f32 = torch.bfloat16, torch.float32
 
 # (M, N, K): the tile of 256 x 256; 128 x 256; 128 x 128, whole and K in three; 64 x 128, whole and K in three;
 # 64 x 64, whole and K split 4 to 16 ways; rounds of 256 x 256 with 128 x 256, 64 x 128 and 64 x 64 beside them;
-# K of one chunk, of fewer bytes than a step and of a whole number of chunks
+# K of one chunk, of fewer bytes than a step and of a whole number of chunks; few tokens, 8 and 16 waves
 SIZES = [(1290, 9400, 650), (2005, 4090, 2001), (1023, 4095, 1001), (2208, 508, 10293), (2050, 9000, 520),
          (411, 2958, 12801), (333, 1001, 2049), (129, 1000, 4000), (118, 70, 8192), (33, 48, 20000),
          (4096, 14336, 900), (3990, 9001, 700), (2000, 9000, 1030), (1290, 9400, 100), (1290, 9400, 40),
-         (1290, 9400, 256), (2005, 4090, 128), (70, 200, 65), (9, 130, 300000 // 16), (16, 14336, 2000)]
+         (1290, 9400, 256), (2005, 4090, 128), (70, 200, 65), (9, 130, 300000 // 16), (16, 14336, 2000),
+         (5, 4096, 9001), (20, 200, 9000)]
 
 
 def _codes(rows, cols, seed):
