@@ -215,11 +215,12 @@ PyObject* int8_gemm(PyObject*, PyObject* const* a, Py_ssize_t n)
 }
 
 // (params, their addresses (buffer of uint64), sizes (buffer of int64), grads, table on the host, on the device,
-//  state kind, m, ms, v, vs, lr, beta1, beta2, eps, weight_decay, step) -> True
+//  state kind, m, ms, v, vs, lr, beta1, beta2, eps, weight_decay, step, the plan's stream) -> True
+// (on another stream than the plan's the wrapper's code also keeps the plan's memory for it)
 PyObject* adamw_multi_step(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    PLAIN(n == 17 && PyList_CheckExact(a[0]) && (PyList_CheckExact(a[3]) || PyTuple_CheckExact(a[3])));
+    PLAIN(n == 18 && PyList_CheckExact(a[0]) && (PyList_CheckExact(a[3]) || PyTuple_CheckExact(a[3])));
     const Py_ssize_t count = PyList_GET_SIZE(a[0]);
     PLAIN(PySequence_Fast_GET_SIZE(a[3]) == count && count > 0);
     const auto* at0 = static_cast<const uint64_t*>(PyLong_AsVoidPtr(a[1]));
@@ -227,7 +228,7 @@ PyObject* adamw_multi_step(PyObject*, PyObject* const* a, Py_ssize_t n)
     PLAIN(at0 && sizes);
     PyObject** grads = PySequence_Fast_ITEMS(a[3]);
     const at::Tensor *host = THPVariable_Check(a[4]) ? &THPVariable_Unpack(a[4]) : nullptr, *dev_table = operand(a[5]);
-    PLAIN(host && dev_table && PyLong_Check(a[6]) && PyLong_Check(a[16]));
+    PLAIN(host && dev_table && PyLong_Check(a[6]) && PyLong_Check(a[16]) && PyLong_Check(a[17]));
     double h[5];
     for (int i = 0; i < 5; ++i) {
         PLAIN(PyFloat_Check(a[11 + i]));
@@ -241,12 +242,12 @@ PyObject* adamw_multi_step(PyObject*, PyObject* const* a, Py_ssize_t n)
     }
     int dev;
     hipStream_t st;
-    PLAIN(place(*dev_table, &st, &dev));
+    PLAIN(place(*dev_table, &st, &dev) && st == static_cast<hipStream_t>(PyLong_AsVoidPtr(a[17])));
     std::vector<const void*> g((size_t)count);
     int gd = -1;
     for (Py_ssize_t i = 0; i < count; ++i) {
         const at::Tensor* p = operand(PyList_GET_ITEM(a[0], i));
-        PLAIN(p && (uint64_t)(uintptr_t)p->data_ptr() == at0[i]);
+        PLAIN(p && (uint64_t)(uintptr_t)p->data_ptr() == at0[i] && p->numel() == sizes[i]);
         if (grads[i] == Py_None) continue;
         const at::Tensor* t = operand(grads[i]);
         PLAIN(t && t->numel() == sizes[i] && t->is_contiguous() && t->get_device() == dev);

@@ -257,7 +257,9 @@ __device__ __forceinline__ void product(v4i& acc, const v4i& b, const v4i& a)
 // leaves: 8192 x 8192 x 8192 in 380 us (2890 TOP/s), whatever the places of
 // reads and loads among the products (375 to 391 us over seven schedules);
 // 4096 x 14336 x 4096 in 190 us, 117 MB of output among it.  The small tiles
-// are bound by the latency of a step, 0.12 us.  Chunks of 64 (half a cache
+// are bound by the direct loads, 35 to 40 bytes a clock and CU at any depth of
+// the ring; one barrier and one wait a chunk instead of two gained nothing.
+// Chunks of 64 (half a cache
 // line a row) took twice the lines from L2: 632 us for 8192 x 8192 x 8192.
 template <typename C, int NI, int NJ, int D, int OCC>
 __global__ __launch_bounds__(256, OCC) void int8_gemm_tile_kernel(Int8Args p, int tiles_m, int tiles_n, int split,

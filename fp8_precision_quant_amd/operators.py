@@ -264,9 +264,8 @@ class AdamWPlan:
         B = self.blocks[-1]
         want = [(torch.float32, B * TILE)] * 2 if kind == STATE_F32 else \
             [(torch.uint8, B * TILE), (torch.float32, B)] * 2
-        if moments is None:
-            moments = tuple(torch.zeros(n, dtype=dt, device=dev) for dt, n in want)
-        moments = tuple(moments)
+        fresh = moments is None
+        moments = tuple(torch.zeros(n, dtype=dt, device=dev) for dt, n in want) if fresh else tuple(moments)
         if len(moments) != len(want):
             raise ValueError("expected %d moment tensors, got %d" % (len(want), len(moments)))
         for i, (t, (dt, n)) in enumerate(zip(moments, want)):
@@ -285,6 +284,8 @@ class AdamWPlan:
             raise Fp8qError(st, "fp8q_adamw_table_fill")
         self._table = self._host.to(dev)
         torch.cuda.current_stream(dev).synchronize()     # a step may run on any stream
+        # what the plan allocated, and the stream that memory belongs to
+        self._home, self._owned = _Call(params[0], None).handle, (self._table, *(moments if fresh else ()))
         self._at = [p.data_ptr() for p in params]
         self._p, self._n = array("Q", self._at), array("q", self.sizes)
         self._at_address, self._sizes_address = self._p.buffer_info()[0], self._n.buffer_info()[0]
@@ -308,7 +309,7 @@ def fp8q_adamw_multi_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor
 
     ``grads``: one contiguous tensor per parameter with as many elements, all bf16 or all fp32; a parameter whose
     entry is None is left as it is.  In a captured graph the hyperparameters, the step number and the addresses of
-    this call are replayed."""
+    this call are replayed; keep the plan as long as the graph."""
     if not isinstance(plan, AdamWPlan):
         raise ValueError("plan must come from fp8q_adamw_plan")
     if len(grads) != len(plan.sizes):
@@ -320,13 +321,13 @@ def fp8q_adamw_multi_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor
         m, ms, v, vs = plan.moments
     if stream is None:
         r = _fast.adamw_multi_step(plan.params, plan._at_address, plan._sizes_address, grads, plan._host, plan._table,
-                                   plan.kind, m, ms, v, vs, lr, beta1, beta2, eps, weight_decay, step)
+                                   plan.kind, m, ms, v, vs, lr, beta1, beta2, eps, weight_decay, step, plan._home)
         if r is not None:
             _done(r, "fp8q_adamw_multi_step")
             return
     call = _Call(plan.params[0], stream)
     tensor = torch.Tensor
-    if list(map(tensor.data_ptr, plan.params)) != plan._at:
+    if list(map(tensor.data_ptr, plan.params)) != plan._at or list(map(tensor.numel, plan.params)) != plan.sizes:
         raise ValueError("a parameter has moved in memory since the plan was made")
     live, sizes = grads, plan.sizes
     if any(g is None for g in grads):
@@ -349,7 +350,11 @@ def fp8q_adamw_multi_step(plan: AdamWPlan, grads: Sequence[Optional[torch.Tensor
     call(_lib.fp8q_adamw_multi_step, "fp8q_adamw_multi_step", plan._host.data_ptr(), plan._table.data_ptr(), plan._at_address,
          ptrs.buffer_info()[0], gd, plan.kind, m.data_ptr(), _ptr(ms), v.data_ptr(), _ptr(vs), lr, beta1, beta2, eps,
          weight_decay, step)
-    call.keep(plan._table)
+    if call.handle != plan._home:
+        # the plan may be dropped before the step has run: its memory then waits for this stream
+        other = call.other or torch.cuda.current_stream(call.dev)
+        for t in plan._owned:
+            t.record_stream(other)
 
 
 # ---------------------------------------------------------------------------

@@ -20,8 +20,8 @@ V = torch.zeros(4)
     (_fast.int8_quant_rows, (F,)), (_fast.int8_quant_rows, ([1.0],)), (_fast.int8_quant_rows, ()),
     (_fast.int8_quant_rows, (torch.zeros(4, 32).to_sparse(),)), (_fast.int8_quant_rows, (torch.zeros(4, 32, device="meta"),)),
     (_fast.int8_gemm, (I8, V, I8, V, None, True)), (_fast.int8_gemm, (None,) * 6), (_fast.int8_gemm, (I8, V)),
-    (_fast.adamw_multi_step, ()), (_fast.adamw_multi_step, (None,) * 17),
-    (_fast.adamw_multi_step, ([], 0, 0, [], *(None,) * 13)), (_fast.adamw_multi_step, ([V], 0, 0, [V], *(None,) * 13)),
+    (_fast.adamw_multi_step, ()), (_fast.adamw_multi_step, (None,) * 18),
+    (_fast.adamw_multi_step, ([], 0, 0, [], *(None,) * 14)), (_fast.adamw_multi_step, ([V], 0, 0, [V], *(None,) * 14)),
 ])
 def test_other_calls_are_left_to_the_wrappers(f, args):
     assert f(*args) is None

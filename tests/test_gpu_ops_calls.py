@@ -67,6 +67,35 @@ def test_adamw(kind, missing):
     _same(run(), run(stream=torch.cuda.current_stream()))
 
 
+@pytest.mark.parametrize("given", [False, True])
+def test_a_dropped_plan_waits_for_its_step(given):
+    """The memory a plan allocated is not handed out again while a step on another stream may still read it."""
+    n = 1 << 20
+    params, grads = [_randn(n, seed=1)], [_randn(n, seed=2)]
+    want = [p.clone() for p in params]
+    fq.fp8q_adamw_multi_step(fq.fp8q_adamw_plan(want), grads, lr=1e-2, step=1)
+    torch.cuda.synchronize()
+    plan = fq.fp8q_adamw_plan(params)
+    owned = {t.data_ptr(): t.numel() * t.element_size() for t in plan._owned}
+    side = torch.cuda.Stream()
+    x = _randn(2048, 2048, seed=3)
+    with torch.cuda.stream(side):
+        for _ in range(50):         # the side stream's own work, in front of the step
+            x = x @ x
+            x = x / x.norm()
+    if given:
+        fq.fp8q_adamw_multi_step(plan, grads, lr=1e-2, step=1, stream=side)
+    else:
+        with torch.cuda.stream(side):
+            fq.fp8q_adamw_multi_step(plan, grads, lr=1e-2, step=1)
+    del plan
+    again = [torch.full((b,), 255, dtype=torch.uint8, device=DEV) for b in owned.values()]
+    reused = not side.query() and any(t.data_ptr() in owned for t in again)
+    side.synchronize()
+    assert not reused
+    _same(tuple(params), tuple(want))
+
+
 def test_plain_calls_run_on_the_current_stream():
     x, w = _randn(2000, 4096, seed=1, dtype=bf16), _randn(4096, seed=2)
     want = fq.fp8q_layer_norm_forward(x, w)
